@@ -17,8 +17,9 @@
  *       UPDATED state.
  * Entry points: the full-sequence scans (plain, fused with the conv, without
  * allocation, or from a given state), the standalone conv, the single-token
- * streaming step, and the gradients of the scans (reverse-mode
- * differentiation of the same steps).
+ * streaming step, the gradients of the scans (reverse-mode differentiation of
+ * the same steps), and the operators around them in a training step
+ * (LayerNorm and its gradients, the conv's gradients, gradient clipping).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -433,6 +434,128 @@ typedef struct {
 
 S6_API int s6_block_step(const s6_block_dims *dims, const s6_block_weights *w, float *x, float *conv_state,
                          float *h_ssm, s6_stream_t stream);
+
+/*
+ * Training-step operators
+ * -----------------------
+ * What surrounds the scan's forward and backward in a training step of a
+ * block: the LayerNorm in front of it and its gradients, the gradients of the
+ * standalone conv (which carry s6_scan_bwd's du to the block's input), and the
+ * norm and clipping of all gradients.  The pages describe the forward of these
+ * steps ("mamba, live", section "what is actually running"); the gradients are
+ * reverse-mode differentiation of it, and the clipping has no counterpart on
+ * the pages.
+ *
+ * These calls own no scratch: where one needs a workspace the caller passes it
+ * (the _workspace function gives its size in bytes, or a negative s6_status for
+ * arguments that the call would refuse).  Its contents before and after the call mean nothing;
+ * it must be 8-byte aligned and not be used by anything else until the call's
+ * work has run.  Calls with different workspaces may run at the same time, on
+ * any streams, and may be captured into graphs without an earlier call.  All sums are made in a
+ * fixed order: the same arguments give the same bits.  Pointers need only
+ * element alignment (wider vectors are used where alignment and sizes allow).
+ * With a NULL or per-thread default stream the tensors must be on the calling
+ * thread's current device.
+ */
+
+/* Sizes and types of a LayerNorm over the rows of [rows, width], row-major. */
+typedef struct {
+    int64_t rows;    /* >= 0 */
+    int64_t width;   /* >= 1, at most 2^24 */
+    int32_t x_dtype; /* s6_dtype of the residual stream (x, s) */
+    int32_t y_dtype; /* s6_dtype of the branch (y, r, dy): x_dtype, or S6_BF16 */
+    float eps;       /* finite, >= 0 */
+} s6_norm_dims;
+
+/*
+ * s6_layernorm_fwd -- LayerNorm of a residual stream, with the add of a
+ * branch's output in front of it (x += out_proj(...) of one block and the
+ * LayerNorm of the next):
+ *
+ *     s = x + r;   m = mean(s);   rstd = 1 / sqrt(mean((s - m)^2) + eps)
+ *     y = (s - m) * rstd * w + b
+ *
+ *  x     [rows,width] x_dtype
+ *  r     [rows,width] y_dtype  branch output; NULL = nothing to add
+ *  w, b  [width]      f32      NULL = ones, zeros
+ *  s     [rows,width] x_dtype  written: x + r (may be x itself); NULL = not
+ *                              wanted.  Must be NULL without r.
+ *  y     [rows,width] y_dtype  written
+ *  mean, rstd [rows]  f32      written, for the backward; NULL = not wanted
+ *
+ * m, rstd and y come from the float32 sum x + r, before its rounding to s.
+ */
+S6_API int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void *r, const float *w, const float *b,
+                            void *s, void *y, float *mean, float *rstd, s6_stream_t stream);
+
+/*
+ * s6_layernorm_bwd -- gradients of s6_layernorm_fwd.  With h = (x - mean) *
+ * rstd and g = w * dy:
+ *
+ *     dx = ds + rstd * (g - mean(g) - h * mean(g * h))
+ *     dw = sum over rows of dy * h;   db = sum over rows of dy
+ *
+ *  x          [rows,width] x_dtype  the normalised stream (the forward's s, or x without r)
+ *  mean, rstd [rows]       f32      as the forward wrote them
+ *  w          [width]      f32      NULL = ones
+ *  dy         [rows,width] y_dtype  gradient with respect to y
+ *  ds         [rows,width] f32      gradient that reaches the stream past the
+ *                                   norm; NULL = zeros
+ *  dx         [rows,width] f32      written (may be ds itself): with respect to
+ *                                   s, and so to x and to r
+ *  dw, db     [width]      f32      written; NULL = not wanted
+ */
+S6_API int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims);
+S6_API int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd,
+                            const float *w, const void *dy, const float *ds, float *dx, float *dw, float *db,
+                            void *workspace, int64_t workspace_bytes, s6_stream_t stream);
+
+/*
+ * causal_conv1d_silu_bwd -- gradients of causal_conv1d_silu_fwd for the loss
+ * sum(dout * out).  dims.d_state is not read; d_inner may be any size.
+ *
+ *  x        [Bt,L,d] io   the forward's input
+ *  conv_w   [d,K] f32, conv_b [d] f32 (NULL = zeros)   as in the forward
+ *  dout     [Bt,L,d]      dout_dtype: S6_F32 (s6_scan_bwd's du) or the I/O dtype
+ *  dx       [Bt,L,d] f32  written
+ *  dconv_w  [d,K]    f32  written
+ *  dconv_b  [d]      f32  written; NULL = not wanted
+ */
+S6_API int64_t causal_conv1d_silu_bwd_workspace(const s6_dims *dims);
+S6_API int causal_conv1d_silu_bwd(const s6_dims *dims, const void *x, const float *conv_w, const float *conv_b,
+                                  const void *dout, int dout_dtype, float *dx, float *dconv_w, float *dconv_b,
+                                  void *workspace, int64_t workspace_bytes, s6_stream_t stream);
+
+/*
+ * s6_grad_norm, s6_grad_clip, s6_clip_grad_norm -- the norm of all gradients
+ * taken as one vector, and their scaling by it:
+ *
+ *     norm = sqrt(sum over tensors and elements of g^2)
+ *     c = min(1, max_norm / (norm + eps));   g <- c * g, in place
+ *
+ * s6_grad_norm computes norm; s6_grad_clip scales by a norm already on the
+ * device (one that ranks have combined, say); s6_clip_grad_norm does both.
+ *
+ *  count    tensors (0: norm is 0); grads, numel, dtypes: HOST arrays of that
+ *           many device pointers, element counts (up to 2^37; 0 allowed) and
+ *           s6_dtypes, read during the call.  Tensors that are scaled must not
+ *           overlap (S6_ERR_INVALID_ARG).
+ *  norm     [1] f32 on the device: written (s6_grad_clip: read)
+ *  max_norm finite, >= 0;  eps finite, >= 0
+ *
+ * The norm holds over float32's whole range: squares do not overflow or vanish
+ * (a norm above the largest float32 is inf).  Where c is 1 nothing is written.
+ * An infinite norm gives c = 0, which turns finite gradients into 0 and
+ * infinite ones into NaN; a NaN norm turns all of them into NaN.
+ */
+S6_API int64_t s6_grad_workspace(int64_t count, const int64_t *numel);
+S6_API int s6_grad_norm(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                        float *norm, void *workspace, int64_t workspace_bytes, s6_stream_t stream);
+S6_API int s6_grad_clip(int64_t count, void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                        const float *norm, float max_norm, float eps, s6_stream_t stream);
+S6_API int s6_clip_grad_norm(int64_t count, void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                             float max_norm, float eps, float *norm, void *workspace, int64_t workspace_bytes,
+                             s6_stream_t stream);
 
 /*
  * s6_device_status -- synchronises `stream`, then reads and clears the

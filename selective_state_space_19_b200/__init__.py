@@ -10,10 +10,12 @@ Functions (same names as the C ABI):
     s6_scan_fwd, s6_conv_scan_fwd, s6_conv_scan_fwd_noalloc, s6_scan_fwd_from_state,
     s6_conv_scan_fwd_from_state, s6_diag_recurrence_fwd, s6_scan_bwd, s6_conv_scan_bwd,
     causal_conv1d_silu_fwd, s6_step, s6_block_step, s6_device_status, s6_status_string, s6_version,
-    s6_debug_carry_fault (tests only)
+    s6_debug_carry_fault (tests only); around them in a training step: s6_layernorm_fwd,
+    s6_layernorm_bwd, causal_conv1d_silu_bwd, s6_grad_norm, s6_grad_clip, s6_clip_grad_norm
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -23,6 +25,8 @@ __all__ = [
     "s6_diag_recurrence_fwd", "S6_DECAY_LIVE", "S6_DECAY_CONST", "s6_scan_bwd", "s6_conv_scan_bwd",
     "causal_conv1d_silu_fwd", "s6_step",
     "s6_block_step", "BlockDims", "BlockWeights", "BLOCK_WEIGHT_KEYS",
+    "s6_layernorm_fwd", "s6_layernorm_bwd", "NormDims", "causal_conv1d_silu_bwd", "s6_grad_norm", "s6_grad_clip",
+    "s6_clip_grad_norm",
     "s6_device_status", "s6_status_string", "s6_version", "s6_debug_carry_fault", "S6_F32", "S6_BF16", "Dims",
 ]
 
@@ -47,6 +51,12 @@ class BlockDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("d_model", ctypes.c_int64), ("d_inner", ctypes.c_int64),
                 ("d_state", ctypes.c_int64), ("dt_rank", ctypes.c_int64), ("conv_width", ctypes.c_int64),
                 ("eps", ctypes.c_float)]
+
+
+class NormDims(ctypes.Structure):
+    """Mirror of ``s6_norm_dims``."""
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 BLOCK_WEIGHT_KEYS = ("ln_w", "ln_b", "in_q", "in_s", "conv_w", "conv_b", "xp_q", "xp_s", "dt_q", "dt_s", "dt_bias",
@@ -101,6 +111,21 @@ def lib() -> ctypes.CDLL:
         L.s6_block_step.argtypes = [ctypes.POINTER(BlockDims), ctypes.POINTER(BlockWeights), _P, _P, _P, _P]
         L.s6_block_step.restype = _I
         L.s6_debug_carry_fault.restype = _I
+        NP, I64, F = ctypes.POINTER(NormDims), ctypes.c_int64, ctypes.c_float
+        L.s6_layernorm_fwd.argtypes = [NP] + [_P] * 9
+        L.s6_layernorm_bwd.argtypes = [NP] + [_P] * 10 + [I64, _P]
+        L.s6_layernorm_bwd_workspace.argtypes = [NP]
+        L.causal_conv1d_silu_bwd.argtypes = [DP, _P, _P, _P, _P, _I, _P, _P, _P, _P, I64, _P]
+        L.causal_conv1d_silu_bwd_workspace.argtypes = [DP]
+        L.s6_grad_norm.argtypes = [I64] + [_P] * 5 + [I64, _P]
+        L.s6_grad_clip.argtypes = [I64] + [_P] * 4 + [F, F, _P]
+        L.s6_clip_grad_norm.argtypes = [I64] + [_P] * 3 + [F, F, _P, _P, I64, _P]
+        L.s6_grad_workspace.argtypes = [I64, _P]
+        for f in (L.s6_layernorm_fwd, L.s6_layernorm_bwd, L.causal_conv1d_silu_bwd, L.s6_grad_norm, L.s6_grad_clip,
+                  L.s6_clip_grad_norm):
+            f.restype = _I
+        for f in (L.s6_layernorm_bwd_workspace, L.causal_conv1d_silu_bwd_workspace, L.s6_grad_workspace):
+            f.restype = I64
         for f in (L.s6_scan_fwd, L.s6_conv_scan_fwd, L.s6_conv_scan_fwd_noalloc, L.s6_scan_fwd_from_state,
                   L.s6_conv_scan_fwd_from_state, L.s6_diag_recurrence_fwd, L.s6_scan_bwd, L.s6_conv_scan_bwd, L.causal_conv1d_silu_fwd, L.s6_step,
                   L.s6_device_status, L.s6_version):
@@ -451,6 +476,215 @@ def s6_block_step(x, conv_state, h_ssm, w, eps=1e-5, stream=None):
                              _ptr(h_ssm, "h_ssm", f32, (Bt, di, N), dev), _stream(stream, dev))
     _check(st, "s6_block_step")
     return x
+
+
+# ------------------------------------------------- training-step operators
+# These pass a workspace that torch allocates on the stream of the call, so calls
+# on several streams, and several captured graphs, do not share one.
+_HERE_NOW = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """A context in which ``dev`` is the current device and ``stream`` (None: its
+    current stream) the current stream, for the launch and for what is allocated."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE_NOW if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _workspace(need, where, dev):
+    if need < 0:
+        raise S6Error(need, where)
+    return _torch().empty(need, dtype=_torch().uint8, device=dev)
+
+
+def _cuda(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtype=None, want_stats=True,
+                     stream=None):
+    """LayerNorm over the last dimension of the residual stream x [..., W], after adding
+    a branch's output r (None: nothing to add).  w, b [W] float32 (None: ones, zeros).
+    The branch type y_dtype (of r and y) is x's, or bfloat16 beside a float32 x; it
+    defaults to r's or y's, else to x's.  s: where to put x + r (x itself is allowed).
+    Returns (y, s, mean, rstd): s is x when there is no r; mean and rstd [...] float32
+    are for s6_layernorm_bwd (None unless want_stats)."""
+    torch = _torch()
+    if _cuda(x, "x").dim() < 1:
+        raise ValueError("x must have a last dimension to normalise")
+    shape, W, dev = x.shape, x.shape[-1], x.device
+    if y_dtype is None:
+        y_dtype = r.dtype if r is not None else y.dtype if y is not None else x.dtype
+    if y_dtype not in (x.dtype, torch.bfloat16):
+        raise TypeError(f"the branch type must be {x.dtype} or bfloat16 beside a {x.dtype} stream, got {y_dtype}")
+    if s is not None and r is None:
+        raise ValueError("s is the sum x + r: it needs r")
+    f32 = torch.float32
+    xc = _io_code(x)
+    yc = xc if y_dtype == x.dtype else S6_BF16
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(shape, dtype=y_dtype, device=dev)
+        if r is not None and s is None:
+            s = torch.empty_like(x)
+        stats = torch.empty((2,) + shape[:-1], dtype=f32, device=dev) if want_stats else (None, None)
+        mean, rstd = stats[0], stats[1]
+        dims = NormDims(x.numel() // W if W else 0, W, xc, yc, float(eps))
+        _check(lib().s6_layernorm_fwd(
+            ctypes.byref(dims), _ptr(x, "x"), _ptr(r, "r", y_dtype, shape, dev), _ptr(w, "w", f32, (W,), dev),
+            _ptr(b, "b", f32, (W,), dev), _ptr(s, "s", x.dtype, shape, dev), _ptr(y, "y", y_dtype, shape, dev),
+            _ptr(mean, "mean"), _ptr(rstd, "rstd"), _stream(None, dev)), "s6_layernorm_fwd")
+    return y, (x if r is None else s), mean, rstd
+
+
+def s6_layernorm_bwd(dy, x, mean, rstd, w=None, ds=None, dx=None, want_params=True, stream=None):
+    """Gradients of s6_layernorm_fwd: x is what was normalised (the forward's s), mean and
+    rstd are its statistics, dy [..., W] is in the branch type; ds [..., W] float32 is the
+    gradient that reaches the stream past the norm (None: zeros), and is added.  dx: where
+    to put the stream's gradient (ds itself is allowed).  Returns a dict of float32
+    tensors: dx [..., W] (with respect to s, and so to x and r), dw and db [W] (None
+    unless want_params)."""
+    torch = _torch()
+    if _cuda(x, "x").dim() < 1:
+        raise ValueError("x must have a last dimension")
+    shape, W, dev = x.shape, x.shape[-1], x.device
+    if _cuda(dy, "dy").dtype not in (x.dtype, torch.bfloat16):
+        raise TypeError(f"dy must be {x.dtype} or bfloat16 beside a {x.dtype} stream, got {dy.dtype}")
+    f32 = torch.float32
+    xc = _io_code(x)
+    dims = NormDims(x.numel() // W if W else 0, W, xc, xc if dy.dtype == x.dtype else S6_BF16, 0.0)
+    L = lib()
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty(shape, dtype=f32, device=dev)
+        dw, db = torch.empty((2, W), dtype=f32, device=dev) if want_params else (None, None)
+        ws = _workspace(L.s6_layernorm_bwd_workspace(ctypes.byref(dims)), "s6_layernorm_bwd", dev)
+        rows = shape[:-1]
+        _check(L.s6_layernorm_bwd(
+            ctypes.byref(dims), _ptr(x, "x"), _ptr(mean, "mean", f32, rows, dev), _ptr(rstd, "rstd", f32, rows, dev),
+            _ptr(w, "w", f32, (W,), dev), _ptr(dy, "dy", dy.dtype, shape, dev), _ptr(ds, "ds", f32, shape, dev),
+            _ptr(dx, "dx", f32, shape, dev), _ptr(dw, "dw"), _ptr(db, "db"), ws.data_ptr(), ws.numel(),
+            _stream(None, dev)), "s6_layernorm_bwd")
+    return {"dx": dx, "dw": dw, "db": db}
+
+
+def causal_conv1d_silu_bwd(x, conv_w, dout, conv_b=None, stream=None):
+    """Gradients of causal_conv1d_silu_fwd for the loss sum(dout * out): dout [Bt, L, d] is
+    float32 (the du of s6_scan_bwd) or x's type.  Returns a dict of float32 tensors: dx
+    [Bt, L, d], dconv_w [d, K], dconv_b [d] (None without conv_b)."""
+    torch = _torch()
+    if _cuda(x, "x").dim() != 3:
+        raise ValueError("x must be [batch, seqlen, d_inner]")
+    Bt, L, d = x.shape
+    K = _cuda(conv_w, "conv_w").shape[-1]
+    dev, f32 = x.device, torch.float32
+    if _cuda(dout, "dout").dtype not in (f32, x.dtype):
+        raise TypeError(f"dout must be float32 or {x.dtype}, got {dout.dtype}")
+    dims = Dims(Bt, L, d, 1, K, _io_code(x))
+    lb = lib()
+    with _on(dev, stream):
+        dx = torch.empty((Bt, L, d), dtype=f32, device=dev)
+        dw = torch.empty((d, K), dtype=f32, device=dev)
+        db = torch.empty((d,), dtype=f32, device=dev) if conv_b is not None else None
+        ws = _workspace(lb.causal_conv1d_silu_bwd_workspace(ctypes.byref(dims)), "causal_conv1d_silu_bwd", dev)
+        _check(lb.causal_conv1d_silu_bwd(
+            ctypes.byref(dims), _ptr(x, "x"), _ptr(conv_w, "conv_w", f32, (d, K), dev),
+            _ptr(conv_b, "conv_b", f32, (d,), dev), _ptr(dout, "dout", dout.dtype, (Bt, L, d), dev), _io_code(dout),
+            _ptr(dx, "dx"), _ptr(dw, "dconv_w"), _ptr(db, "dconv_b"), ws.data_ptr(), ws.numel(),
+            _stream(None, dev)), "causal_conv1d_silu_bwd")
+    return {"dx": dx, "dconv_w": dw, "dconv_b": db}
+
+
+class _GradList:
+    """The tensors of a call as the host arrays that the library reads."""
+
+    def __init__(self, grads, device=None):
+        torch = _torch()
+        if isinstance(grads, torch.Tensor):
+            grads = (grads,)
+        elif isinstance(grads, dict):
+            grads = grads.values()
+        ts = [g for g in grads if g is not None]
+        codes = {torch.float32: S6_F32, torch.bfloat16: S6_BF16}
+        dev = _cuda(ts[0], "grads[0]").device if ts else device
+        if ts and device is not None and dev != device:
+            raise ValueError(f"the gradients are on {dev}, norm on {device}")
+        for i, t in enumerate(ts):
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev and t.is_contiguous()):
+                _ptr(t, f"grads[{i}]", device=dev)  # raises what is wrong
+            if t.dtype not in codes:
+                raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {t.dtype}")
+        n = len(ts)
+        self.device, self.count = dev, n
+        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
+        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in ts])
+        self.codes = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in ts])
+
+
+def _norm_out(norm, dev):
+    torch = _torch()
+    if norm is None:
+        return torch.empty((), dtype=torch.float32, device=dev)
+    _ptr(norm, "norm", torch.float32, None, dev)
+    if norm.numel() != 1:
+        raise ValueError(f"norm has {norm.numel()} elements, expected 1")
+    return norm
+
+
+def _norm_device(norm, dev):
+    if dev is not None:
+        return dev
+    torch = _torch()
+    return norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def s6_grad_norm(grads, norm=None, stream=None):
+    """The norm of all gradients taken as one vector: a float32 scalar on the device.
+    grads: tensors (a list, or the dict of a backward call; None entries are left out),
+    float32 or bfloat16, contiguous, on one device.  norm: where to put it."""
+    g = _GradList(grads, norm.device if norm is not None else None)
+    dev = _norm_device(norm, g.device)
+    L = lib()
+    with _on(dev, stream):
+        norm = _norm_out(norm, dev)
+        ws = _workspace(L.s6_grad_workspace(g.count, g.numel), "s6_grad_norm", dev)
+        _check(L.s6_grad_norm(g.count, g.ptrs, g.numel, g.codes, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _stream(None, dev)), "s6_grad_norm")
+    return norm
+
+
+def s6_grad_clip(grads, norm, max_norm, eps=1e-6, stream=None):
+    """Scales the gradients in place by min(1, max_norm / (norm + eps)), for a norm that is
+    on the device already (one that ranks have combined, say).  No two tensors may overlap."""
+    g = _GradList(grads, _cuda(norm, "norm").device)
+    dev = norm.device
+    with _on(dev, stream):
+        norm = _norm_out(norm, dev)
+        _check(lib().s6_grad_clip(g.count, g.ptrs, g.numel, g.codes, norm.data_ptr(), float(max_norm), float(eps),
+                                  _stream(None, dev)), "s6_grad_clip")
+
+
+def s6_clip_grad_norm(grads, max_norm, eps=1e-6, norm=None, stream=None):
+    """s6_grad_norm and s6_grad_clip in one call: scales the gradients in place by
+    min(1, max_norm / (norm + eps)) and returns norm, as it was before."""
+    g = _GradList(grads, norm.device if norm is not None else None)
+    dev = _norm_device(norm, g.device)
+    L = lib()
+    with _on(dev, stream):
+        norm = _norm_out(norm, dev)
+        ws = _workspace(L.s6_grad_workspace(g.count, g.numel), "s6_clip_grad_norm", dev)
+        _check(L.s6_clip_grad_norm(g.count, g.ptrs, g.numel, g.codes, float(max_norm), float(eps), norm.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), _stream(None, dev)), "s6_clip_grad_norm")
+    return norm
 
 
 def s6_device_status(stream=None, device=None) -> int:

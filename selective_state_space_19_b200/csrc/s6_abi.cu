@@ -13,6 +13,7 @@
 
 #include "s6.h"
 #include "s6_common.cuh"
+#include "s6_host.cuh"
 #include "s6_conv.cuh"
 #include "s6_scan.cuh"
 #include "s6_step.cuh"
@@ -22,6 +23,7 @@
 
 namespace {
 
+using namespace s6::host;
 using s6::ScanArgs;
 
 constexpr int kMaxState = 16;
@@ -63,11 +65,6 @@ bool make_map_3d(CUtensorMap *map, const void *base, int io, int64_t Bt, int64_t
     return r == CUDA_SUCCESS;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-size_t io_size(int io) { return io == S6_BF16 ? 2 : 4; }
-
 // ------------------------------------------------------------ validation
 int check_dims(const s6_dims *dims, bool need_L, bool need_K) {
     if (!dims)
@@ -83,47 +80,6 @@ int check_dims(const s6_dims *dims, bool need_L, bool need_K) {
     // 32-bit index arithmetic inside the kernels (per-sequence offsets stay 64-bit)
     if (dims->d_inner > (1 << 30) || dims->batch > (1 << 30) || (need_L && dims->seqlen > (1 << 30)))
         return S6_ERR_UNSUPPORTED;
-    return S6_OK;
-}
-
-int launch_status(cudaError_t e) { return e == cudaSuccess ? S6_OK : S6_ERR_CUDA; }
-
-// Every entry point restores the calling thread's current device before it
-// returns: use_stream_device below may switch it to the stream's device.
-struct DeviceRestore {
-    int prev = -1;
-    DeviceRestore() {
-        if (cudaGetDevice(&prev) != cudaSuccess)
-            prev = -1;
-    }
-    ~DeviceRestore() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev)
-            cudaSetDevice(prev);
-    }
-    DeviceRestore(const DeviceRestore &) = delete;
-    DeviceRestore &operator=(const DeviceRestore &) = delete;
-};
-
-// Make the device that owns `stream` current for this library's runtime before
-// any launch (the caller's framework may have selected it through another
-// runtime instance in the same process).  The legacy and per-thread default
-// streams keep the current device.
-int use_stream_device(cudaStream_t stream) {
-    if (stream == nullptr || stream == cudaStreamLegacy || stream == cudaStreamPerThread)
-        return S6_OK;
-    // a stream being captured into a graph: the capture already runs on the
-    // current device, and device queries on it would invalidate the capture
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess)
-        return S6_ERR_CUDA;
-    if (cap != cudaStreamCaptureStatusNone)
-        return S6_OK;
-    int dev = -1, cur = -1;
-    if (cudaStreamGetDevice(stream, &dev) != cudaSuccess || cudaGetDevice(&cur) != cudaSuccess)
-        return S6_ERR_CUDA;
-    if (dev != cur && cudaSetDevice(dev) != cudaSuccess)
-        return S6_ERR_CUDA;
     return S6_OK;
 }
 
@@ -173,19 +129,6 @@ struct FixedScratch {
     void *ptr;
     size_t bytes;
 };
-
-int device_sm_count() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-        return 148;
-    if (!cached[dev]) {
-        int n = 0;
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        cached[dev] = n > 0 ? n : 148;
-    }
-    return cached[dev];
-}
 
 size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
@@ -978,7 +921,7 @@ int fwd_ckpt_common(const s6_dims *dims, bool conv, const void *x, const float *
 
 extern "C" {
 
-int s6_version(void) { return (1 << 16) | 0; }
+int s6_version(void) { return (1 << 16) | 1; }
 
 const char *s6_status_string(int status) {
     switch (status) {

@@ -1,0 +1,610 @@
+// s6_train.cu -- the training-step operators around the scan, declared in
+// include/s6.h: LayerNorm forward and backward, the conv's backward, the norm
+// and the clipping of gradients.  Argument checks, choice of kernel and launch;
+// the arithmetic is in s6_norm.cuh, s6_conv_bwd.cuh and s6_grads.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+
+#include "s6.h"
+#include "s6_common.cuh"
+#include "s6_conv_bwd.cuh"
+#include "s6_grads.cuh"
+#include "s6_host.cuh"
+#include "s6_norm.cuh"
+#include "s6_vec.cuh"
+
+namespace {
+
+using namespace s6::host;
+using bf16 = __nv_bfloat16;
+
+// The grids below are sized for the 148 SMs of a B200 and do not ask the device,
+// so the workspace of a call depends on its sizes alone.  Blocks never wait for
+// one another: on fewer SMs they only take longer.
+constexpr int64_t kSMs = 148;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A kernel whose blocks may start while the one before it on the stream drains;
+// it waits for that one's results itself (cudaGridDependencySynchronize).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+int sum_parts(const float *part, int64_t rows, int64_t cols, int segs, int segs0, float *out0, float *out1,
+              cudaStream_t st) {
+    s6::SumPartsArgs a;
+    a.part = part;
+    a.rows = static_cast<int>(rows);
+    a.cols = static_cast<int>(cols);
+    a.segs = segs;
+    a.segs0 = segs0;
+    a.out0 = out0;
+    a.out1 = out1;
+    return launch_status(launch_after(s6::s6_sum_parts_kernel, dim3(static_cast<unsigned>(ceil_div(cols * segs, 32))),
+                                      32 * s6::kSumPartsWarps, st, a));
+}
+
+int check_workspace(const void *ws, int64_t bytes, int64_t need) {
+    if (need > 0 && (!ws || bytes < need))
+        return S6_ERR_INVALID_ARG;
+    return ws && !aligned_to(ws, 8) ? S6_ERR_ALIGNMENT : S6_OK;
+}
+
+// ---------------------------------------------------------------- LayerNorm
+int check_norm_dims(const s6_norm_dims *dims) {
+    if (!dims || dims->rows < 0 || dims->width < 1 || !std::isfinite(dims->eps) || dims->eps < 0.0f)
+        return S6_ERR_INVALID_ARG;
+    const bool types = (dims->x_dtype == S6_F32 && (dims->y_dtype == S6_F32 || dims->y_dtype == S6_BF16)) ||
+                       (dims->x_dtype == S6_BF16 && dims->y_dtype == S6_BF16);
+    if (!types || dims->width > (1 << 24) || dims->rows > (int64_t(1) << 40))
+        return S6_ERR_UNSUPPORTED;
+    return S6_OK;
+}
+
+struct NormPlan {
+    int warps;      // warps that share a row; 1: a row a warp, kNormBlockWarps rows a block
+    int threads;
+    int64_t blocks;
+};
+
+// One warp a row up to 512 elements, above that as many warps as hold the row at
+// 16 elements a thread.  About `resident` warps for each SM, which walk the rows.
+NormPlan norm_plan(int64_t rows, int64_t width, int resident) {
+    NormPlan p;
+    p.warps = static_cast<int>(ceil_div(width, s6::kNormPerWarp));
+    if (p.warps == 1) {
+        p.threads = 32 * s6::kNormBlockWarps;
+        p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps), kSMs * resident / s6::kNormBlockWarps);
+    } else {
+        p.threads = 32 * p.warps;
+        p.blocks = std::min(rows, kSMs * std::max<int64_t>(1, resident / p.warps));
+    }
+    return p;
+}
+
+constexpr int kNormFwdResident = 32, kNormBwdResident = 16;
+
+// Runs of rows of the wide backward's second kernel: enough blocks to fill the
+// SMs at its 128-thread blocks, whatever the vector width.
+int64_t norm_wide_runs(int64_t rows, int64_t width) {
+    const int64_t tiles = ceil_div(width, s6::kNormColThreads * 4);
+    return std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
+}
+
+template <typename X, typename Y, int V, int NV>
+int norm_fwd_nv(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(p.blocks));
+    if (p.warps == 1)
+        s6::s6_layernorm_fwd_kernel<X, Y, V, NV, true><<<grid, p.threads, 0, st>>>(a);
+    else
+        s6::s6_layernorm_fwd_kernel<X, Y, V, NV, false><<<grid, p.threads, 0, st>>>(a);
+    return launch_status(cudaGetLastError());
+}
+
+template <typename X, typename Y, int V, int NV>
+int norm_bwd_nv(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(p.blocks));
+    if (p.warps == 1)
+        s6::s6_layernorm_bwd_kernel<X, Y, V, NV, true><<<grid, p.threads, 0, st>>>(a);
+    else
+        s6::s6_layernorm_bwd_kernel<X, Y, V, NV, false><<<grid, p.threads, 0, st>>>(a);
+    return launch_status(cudaGetLastError());
+}
+
+template <typename X, typename Y, int V>
+int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
+    if (a.width > s6::kNormMaxWidth) {
+        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * 4);
+        s6::s6_layernorm_fwd_wide_kernel<X, Y, V>
+            <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a);
+        return launch_status(cudaGetLastError());
+    }
+    const NormPlan p = norm_plan(a.rows, a.width, kNormFwdResident);
+    const int64_t nv = ceil_div(a.width, V * 32 * p.warps);
+    if constexpr (V == 4) {
+        if (nv == 1)
+            return norm_fwd_nv<X, Y, 4, 1>(a, p, st);
+        if (nv == 2)
+            return norm_fwd_nv<X, Y, 4, 2>(a, p, st);
+        if (nv == 3)
+            return norm_fwd_nv<X, Y, 4, 3>(a, p, st);
+        return norm_fwd_nv<X, Y, 4, 4>(a, p, st);
+    } else {
+        if (nv <= 4)
+            return norm_fwd_nv<X, Y, 1, 4>(a, p, st);
+        if (nv <= 8)
+            return norm_fwd_nv<X, Y, 1, 8>(a, p, st);
+        return norm_fwd_nv<X, Y, 1, 16>(a, p, st);
+    }
+}
+
+template <typename X, typename Y, int V>
+int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db, cudaStream_t st) {
+    s6::NormBwdArgs a = in;
+    float *part = static_cast<float *>(workspace);
+    const bool params = dw || db;
+    int64_t parts = 0;
+    if (a.width > s6::kNormMaxWidth) {
+        float2 *sums = static_cast<float2 *>(workspace);
+        part = static_cast<float *>(workspace) + 2 * a.rows;
+        parts = norm_wide_runs(a.rows, a.width);
+        a.part = params ? part : nullptr;
+        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * 4);
+        s6::s6_layernorm_bwd_wide_sums_kernel<X, Y, V>
+            <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a, sums);
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.width, s6::kNormColThreads * V)),
+                        static_cast<unsigned>(parts));
+        s6::s6_layernorm_bwd_wide_cols_kernel<X, Y, V><<<grid, s6::kNormColThreads, 0, st>>>(a, sums);
+    } else {
+        const NormPlan p = norm_plan(a.rows, a.width, kNormBwdResident);
+        const int64_t nv = ceil_div(a.width, V * 32 * p.warps);
+        parts = p.blocks;
+        a.part = params ? part : nullptr;
+        int rc;
+        if constexpr (V == 4)
+            rc = nv == 1   ? norm_bwd_nv<X, Y, 4, 1>(a, p, st)
+                 : nv == 2 ? norm_bwd_nv<X, Y, 4, 2>(a, p, st)
+                 : nv == 3 ? norm_bwd_nv<X, Y, 4, 3>(a, p, st)
+                           : norm_bwd_nv<X, Y, 4, 4>(a, p, st);
+        else
+            rc = nv <= 4   ? norm_bwd_nv<X, Y, 1, 4>(a, p, st)
+                 : nv <= 8 ? norm_bwd_nv<X, Y, 1, 8>(a, p, st)
+                           : norm_bwd_nv<X, Y, 1, 16>(a, p, st);
+        if (rc != S6_OK)
+            return rc;
+    }
+    const int rc = launch_status(cudaGetLastError());
+    if (rc != S6_OK || !params)
+        return rc;
+    return sum_parts(part, parts, a.width, 2, 1, dw, db, st);
+}
+
+// Vectors of 4 elements where every row starts on one; single elements otherwise.
+bool vec4(int64_t width, const void *const *io, const size_t *size, int n) {
+    if (width % 4 != 0)
+        return false;
+    for (int i = 0; i < n; ++i)
+        if (io[i] && !aligned_to(io[i], 4 * size[i]))
+            return false;
+    return true;
+}
+
+// -------------------------------------------------------------------- conv
+struct ConvBwdPlan {
+    int64_t tiles, blocks_y, run, runs;
+};
+
+constexpr int64_t kConvBwdBlocks = kSMs * 4;  // resident blocks of 4 warps
+constexpr int64_t kConvBwdMinRun = 16;        // tokens; shorter runs read more rows twice than they save
+
+int64_t conv_bwd_blocks_y(int64_t d, int64_t channels) {
+    return std::max<int64_t>(1, kConvBwdBlocks / ceil_div(d, channels));
+}
+
+// One run of tokens for each warp where the warps outnumber the sequences, else
+// about four, so that the last ones to finish are short.
+ConvBwdPlan conv_bwd_plan(int64_t Bt, int64_t L, int64_t d, int V) {
+    ConvBwdPlan p;
+    p.tiles = ceil_div(d, 32 * V);
+    p.blocks_y = conv_bwd_blocks_y(d, 32 * V);
+    const int64_t warps = p.blocks_y * s6::kConvBwdWarps;
+    const int64_t want = Bt < warps ? warps / Bt : ceil_div(4 * warps, Bt);
+    p.run = std::max(ceil_div(L, want), std::min(L, kConvBwdMinRun));
+    p.runs = ceil_div(L, p.run);
+    p.blocks_y = std::min(p.blocks_y, ceil_div(Bt * p.runs, s6::kConvBwdWarps));
+    return p;
+}
+
+template <typename X, typename G, int V, int K>
+int conv_bwd_k(const s6::ConvBwdArgs &a, const ConvBwdPlan &p, float *dconv_w, float *dconv_b, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.blocks_y));
+    s6::s6_conv_silu_bwd_kernel<X, G, V, K><<<grid, 32 * s6::kConvBwdWarps, 0, st>>>(a);
+    const int rc = launch_status(cudaGetLastError());
+    if (rc != S6_OK)
+        return rc;
+    return sum_parts(a.part, p.blocks_y, a.d, K + 1, K, dconv_w, dconv_b, st);
+}
+
+template <typename X, typename G, int V>
+int conv_bwd_v(const s6::ConvBwdArgs &in, int64_t K, float *dconv_w, float *dconv_b, cudaStream_t st) {
+    s6::ConvBwdArgs a = in;
+    const ConvBwdPlan p = conv_bwd_plan(a.Bt, a.L, a.d, V);
+    a.run = static_cast<int>(p.run);
+    a.runs = static_cast<int>(p.runs);
+    if (K == 2)
+        return conv_bwd_k<X, G, V, 2>(a, p, dconv_w, dconv_b, st);
+    if (K == 3)
+        return conv_bwd_k<X, G, V, 3>(a, p, dconv_w, dconv_b, st);
+    return conv_bwd_k<X, G, V, 4>(a, p, dconv_w, dconv_b, st);
+}
+
+template <typename X, typename G>
+int conv_bwd_io(const s6::ConvBwdArgs &a, int64_t K, float *dconv_w, float *dconv_b, cudaStream_t st) {
+    for (int V = 4; V >= 2; V /= 2)
+        if (a.d % V == 0 && aligned_to(a.x, V * sizeof(X)) && aligned_to(a.dout, V * sizeof(G)) &&
+            aligned_to(a.dx, V * sizeof(float)))
+            return V == 4 ? conv_bwd_v<X, G, 4>(a, K, dconv_w, dconv_b, st)
+                          : conv_bwd_v<X, G, 2>(a, K, dconv_w, dconv_b, st);
+    return conv_bwd_v<X, G, 1>(a, K, dconv_w, dconv_b, st);
+}
+
+int check_conv_bwd_dims(const s6_dims *dims) {
+    if (!dims || dims->batch < 0 || dims->seqlen < 0 || dims->d_inner < 1)
+        return S6_ERR_INVALID_ARG;
+    if ((dims->io_dtype != S6_F32 && dims->io_dtype != S6_BF16) || dims->conv_width < 2 || dims->conv_width > 4 ||
+        dims->d_inner > (1 << 30) || dims->batch > (1 << 30) || dims->seqlen > (1 << 30))
+        return S6_ERR_UNSUPPORTED;
+    return S6_OK;
+}
+
+// --------------------------------------------------------------- gradients
+constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^24 chunks of one tensor
+
+// Checks a list; `write`: the tensors are written, so no two may share memory.
+int check_grads(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, bool write) {
+    if (count < 0 || (count > 0 && (!grads || !numel || !dtypes)))
+        return S6_ERR_INVALID_ARG;
+    if (count > (int64_t(1) << 24))
+        return S6_ERR_UNSUPPORTED;
+    for (int64_t i = 0; i < count; ++i) {
+        if (dtypes[i] != S6_F32 && dtypes[i] != S6_BF16)
+            return S6_ERR_UNSUPPORTED;
+        if (numel[i] < 0 || (numel[i] > 0 && !grads[i]))
+            return S6_ERR_INVALID_ARG;
+        if (numel[i] > kGradMaxNumel)
+            return S6_ERR_UNSUPPORTED;
+        if (!aligned_to(grads[i], io_size(dtypes[i])))
+            return S6_ERR_ALIGNMENT;
+    }
+    if (!write || count < 2)
+        return S6_OK;
+    struct Range {
+        uintptr_t at, end;
+    };
+    Range *r = static_cast<Range *>(std::malloc(sizeof(Range) * static_cast<size_t>(count)));
+    if (!r)
+        return S6_ERR_INVALID_ARG;
+    size_t n = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (numel[i] > 0) {
+            r[n].at = reinterpret_cast<uintptr_t>(grads[i]);
+            r[n].end = r[n].at + static_cast<size_t>(numel[i]) * io_size(dtypes[i]);
+            ++n;
+        }
+    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.at < b.at; });
+    bool apart = true;
+    for (size_t i = 1; i < n; ++i)
+        apart = apart && r[i].at >= r[i - 1].end;
+    std::free(r);
+    return apart ? S6_OK : S6_ERR_INVALID_ARG;
+}
+
+// Walks a list in tables of at most M tensors (and few enough chunks to count in
+// an int) and calls fn(table) for each.
+template <int M, typename Fn>
+int for_tables(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, Fn fn) {
+    s6::GradTable<M> t;
+    t.tensors = t.chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (numel[i] == 0)
+            continue;
+        const int chunks = static_cast<int>(ceil_div(numel[i], s6::kGradChunk));  // at most 2^24 (check_grads)
+        if (t.tensors == M || t.chunks + chunks > (1 << 30)) {
+            const int rc = fn(t);
+            if (rc != S6_OK)
+                return rc;
+            t.tensors = t.chunks = 0;
+        }
+        t.chunks += chunks;
+        t.ptr[t.tensors] = reinterpret_cast<void *>(reinterpret_cast<uintptr_t>(grads[i]) |
+                                                    (dtypes[i] == S6_BF16 ? 1u : 0u));
+        t.n[t.tensors] = numel[i];
+        t.end[t.tensors] = t.chunks;
+        ++t.tensors;
+    }
+    return t.tensors ? fn(t) : S6_OK;
+}
+
+unsigned grad_grid(int chunks) { return static_cast<unsigned>(std::min(chunks, s6::kGradMaxBlocks)); }
+
+template <int M>
+int grads_run(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, bool squares,
+              bool scale, s6::GradScaleArgs a, double *part, cudaStream_t st) {
+    int rc = S6_OK;
+    if (squares) {
+        int parts = 0;
+        rc = for_tables<M>(count, grads, numel, dtypes, [&](const s6::GradTable<M> &t) {
+            const unsigned grid = grad_grid(t.chunks);
+            s6::s6_grad_square_kernel<M><<<grid, s6::kGradThreads, 0, st>>>(t, part + parts);
+            parts += static_cast<int>(grid);
+            return launch_status(cudaGetLastError());
+        });
+        if (rc != S6_OK)
+            return rc;
+        a.part = part;
+        a.parts = parts;
+    }
+    bool launched = false;
+    if (scale)
+        rc = for_tables<M>(count, grads, numel, dtypes, [&](const s6::GradTable<M> &t) {
+            const cudaError_t e = launch_after(s6::s6_grad_scale_kernel<M>, dim3(grad_grid(t.chunks)),
+                                               s6::kGradThreads, st, t, a);
+            launched = true;
+            a.norm_out = nullptr;  // the first launch writes it
+            return launch_status(e);
+        });
+    if (rc == S6_OK && !launched && a.norm_out) {
+        s6::GradTable<s6::kGradFew> none;
+        none.tensors = none.chunks = 0;
+        rc = launch_status(launch_after(s6::s6_grad_scale_kernel<s6::kGradFew>, dim3(1), s6::kGradThreads, st, none, a));
+    }
+    return rc;
+}
+
+int grads_common(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, bool squares,
+                 bool scale, const float *norm_in, float *norm_out, float max_norm, float eps, void *workspace,
+                 int64_t workspace_bytes, s6_stream_t stream) {
+    int rc = check_grads(count, grads, numel, dtypes, scale);
+    if (rc != S6_OK)
+        return rc;
+    if (squares ? !norm_out : !norm_in)
+        return S6_ERR_INVALID_ARG;
+    if (scale && (!std::isfinite(max_norm) || max_norm < 0.0f || !std::isfinite(eps) || eps < 0.0f))
+        return S6_ERR_INVALID_ARG;
+    if (!aligned_to(norm_in, 4) || !aligned_to(norm_out, 4))
+        return S6_ERR_ALIGNMENT;
+    if (squares) {
+        rc = check_workspace(workspace, workspace_bytes, s6_grad_workspace(count, numel));
+        if (rc != S6_OK)
+            return rc;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (use_stream_device(st) != S6_OK)
+        return S6_ERR_CUDA;
+    s6::GradScaleArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.norm_in = norm_in;
+    a.norm_out = norm_out;
+    a.max_norm = max_norm;
+    a.eps = eps;
+    double *part = static_cast<double *>(workspace);
+    return count <= s6::kGradFew
+               ? grads_run<s6::kGradFew>(count, grads, numel, dtypes, squares, scale, a, part, st)
+               : grads_run<s6::kGradTensors>(count, grads, numel, dtypes, squares, scale, a, part, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void *r, const float *w, const float *b, void *s,
+                     void *y, float *mean, float *rstd, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    const int rc = check_norm_dims(dims);
+    if (rc != S6_OK || dims->rows == 0)
+        return rc;
+    if (!x || !y || (!r && s))
+        return S6_ERR_INVALID_ARG;
+    const size_t sx = io_size(dims->x_dtype), sy = io_size(dims->y_dtype);
+    if (!aligned_to(x, sx) || !aligned_to(s, sx) || !aligned_to(r, sy) || !aligned_to(y, sy) || !aligned_to(w, 4) ||
+        !aligned_to(b, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return S6_ERR_ALIGNMENT;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (use_stream_device(st) != S6_OK)
+        return S6_ERR_CUDA;
+    s6::NormFwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = dims->rows;
+    a.width = static_cast<int>(dims->width);
+    a.eps = dims->eps;
+    a.inv_w = static_cast<float>(1.0 / static_cast<double>(dims->width));
+    a.x = x;
+    a.r = r;
+    a.w = w;
+    a.b = b;
+    a.s = s;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    const void *io[] = {x, s, r, y};
+    const size_t size[] = {sx, sx, sy, sy};
+    const bool v4 = vec4(dims->width, io, size, 4);
+    if (dims->x_dtype == S6_BF16)
+        return v4 ? norm_fwd_v<bf16, bf16, 4>(a, st) : norm_fwd_v<bf16, bf16, 1>(a, st);
+    if (dims->y_dtype == S6_BF16)
+        return v4 ? norm_fwd_v<float, bf16, 4>(a, st) : norm_fwd_v<float, bf16, 1>(a, st);
+    return v4 ? norm_fwd_v<float, float, 4>(a, st) : norm_fwd_v<float, float, 1>(a, st);
+}
+
+int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims) {
+    const int rc = check_norm_dims(dims);
+    if (rc != S6_OK || dims->rows == 0)
+        return rc;
+    const int64_t row = 2 * dims->width * static_cast<int64_t>(sizeof(float));
+    if (dims->width > s6::kNormMaxWidth)
+        return dims->rows * static_cast<int64_t>(sizeof(float2)) + norm_wide_runs(dims->rows, dims->width) * row;
+    return norm_plan(dims->rows, dims->width, kNormBwdResident).blocks * row;
+}
+
+int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd, const float *w,
+                     const void *dy, const float *ds, float *dx, float *dw, float *db, void *workspace,
+                     int64_t workspace_bytes, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    int rc = check_norm_dims(dims);
+    if (rc != S6_OK)
+        return rc;
+    const size_t sx = io_size(dims->x_dtype), sy = io_size(dims->y_dtype);
+    if (dims->rows > 0 && (!x || !mean || !rstd || !dy || !dx))
+        return S6_ERR_INVALID_ARG;
+    if (!aligned_to(x, sx) || !aligned_to(dy, sy) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
+        !aligned_to(w, 4) || !aligned_to(ds, 4) || !aligned_to(dx, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4))
+        return S6_ERR_ALIGNMENT;
+    rc = check_workspace(workspace, workspace_bytes, s6_layernorm_bwd_workspace(dims));
+    if (rc != S6_OK)
+        return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (use_stream_device(st) != S6_OK)
+        return S6_ERR_CUDA;
+    if (dims->rows == 0) {  // sums over no rows
+        const size_t bytes = sizeof(float) * static_cast<size_t>(dims->width);
+        if ((dw && cudaMemsetAsync(dw, 0, bytes, st) != cudaSuccess) ||
+            (db && cudaMemsetAsync(db, 0, bytes, st) != cudaSuccess))
+            return S6_ERR_CUDA;
+        return S6_OK;
+    }
+    s6::NormBwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = dims->rows;
+    a.width = static_cast<int>(dims->width);
+    a.inv_w = static_cast<float>(1.0 / static_cast<double>(dims->width));
+    a.x = x;
+    a.dy = dy;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.w = w;
+    a.ds = ds;
+    a.dx = dx;
+    const void *io[] = {x, dy, ds, dx};
+    const size_t size[] = {sx, sy, 4, 4};
+    const bool v4 = vec4(dims->width, io, size, 4);
+    if (dims->x_dtype == S6_BF16)
+        return v4 ? norm_bwd_v<bf16, bf16, 4>(a, workspace, dw, db, st)
+                  : norm_bwd_v<bf16, bf16, 1>(a, workspace, dw, db, st);
+    if (dims->y_dtype == S6_BF16)
+        return v4 ? norm_bwd_v<float, bf16, 4>(a, workspace, dw, db, st)
+                  : norm_bwd_v<float, bf16, 1>(a, workspace, dw, db, st);
+    return v4 ? norm_bwd_v<float, float, 4>(a, workspace, dw, db, st)
+              : norm_bwd_v<float, float, 1>(a, workspace, dw, db, st);
+}
+
+int64_t causal_conv1d_silu_bwd_workspace(const s6_dims *dims) {
+    const int rc = check_conv_bwd_dims(dims);
+    if (rc != S6_OK || dims->batch == 0 || dims->seqlen == 0)
+        return rc;
+    // the widest channel tile has the most blocks that share it
+    return conv_bwd_blocks_y(dims->d_inner, 128) * (dims->conv_width + 1) * dims->d_inner *
+           static_cast<int64_t>(sizeof(float));
+}
+
+int causal_conv1d_silu_bwd(const s6_dims *dims, const void *x, const float *conv_w, const float *conv_b,
+                           const void *dout, int dout_dtype, float *dx, float *dconv_w, float *dconv_b,
+                           void *workspace, int64_t workspace_bytes, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    int rc = check_conv_bwd_dims(dims);
+    if (rc != S6_OK)
+        return rc;
+    if (dout_dtype != S6_F32 && dout_dtype != dims->io_dtype)
+        return S6_ERR_UNSUPPORTED;
+    const int64_t Bt = dims->batch, L = dims->seqlen, d = dims->d_inner, K = dims->conv_width;
+    const bool empty = Bt == 0 || L == 0;
+    if (!conv_w || !dconv_w || (!empty && (!x || !dout || !dx)))
+        return S6_ERR_INVALID_ARG;
+    if (!aligned_to(x, io_size(dims->io_dtype)) || !aligned_to(dout, io_size(dout_dtype)) || !aligned_to(dx, 4) ||
+        !aligned_to(conv_w, 4) || !aligned_to(conv_b, 4) || !aligned_to(dconv_w, 4) || !aligned_to(dconv_b, 4))
+        return S6_ERR_ALIGNMENT;
+    rc = check_workspace(workspace, workspace_bytes, causal_conv1d_silu_bwd_workspace(dims));
+    if (rc != S6_OK)
+        return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (use_stream_device(st) != S6_OK)
+        return S6_ERR_CUDA;
+    if (empty) {  // sums over no tokens
+        if (cudaMemsetAsync(dconv_w, 0, sizeof(float) * static_cast<size_t>(d * K), st) != cudaSuccess ||
+            (dconv_b && cudaMemsetAsync(dconv_b, 0, sizeof(float) * static_cast<size_t>(d), st) != cudaSuccess))
+            return S6_ERR_CUDA;
+        return S6_OK;
+    }
+    s6::ConvBwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.Bt = static_cast<int>(Bt);
+    a.L = static_cast<int>(L);
+    a.d = static_cast<int>(d);
+    a.x = x;
+    a.dout = dout;
+    a.conv_w = conv_w;
+    a.conv_b = conv_b;
+    a.dx = dx;
+    a.part = static_cast<float *>(workspace);
+    if (dims->io_dtype == S6_F32)
+        return conv_bwd_io<float, float>(a, K, dconv_w, dconv_b, st);
+    return dout_dtype == S6_F32 ? conv_bwd_io<bf16, float>(a, K, dconv_w, dconv_b, st)
+                                : conv_bwd_io<bf16, bf16>(a, K, dconv_w, dconv_b, st);
+}
+
+int64_t s6_grad_workspace(int64_t count, const int64_t *numel) {
+    if (count < 0 || (count > 0 && !numel))
+        return S6_ERR_INVALID_ARG;
+    // one float64 for each block of each launch: a launch ends with a full table, or
+    // with more than 2^29 chunks
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (numel[i] < 0)
+            return S6_ERR_INVALID_ARG;
+        if (numel[i] > kGradMaxNumel)
+            return S6_ERR_UNSUPPORTED;
+        chunks += ceil_div(numel[i], s6::kGradChunk);
+    }
+    const int64_t launches = count / (count <= s6::kGradFew ? s6::kGradFew : s6::kGradTensors) + 1 + (chunks >> 29);
+    return launches * s6::kGradMaxBlocks * static_cast<int64_t>(sizeof(double));
+}
+
+int s6_grad_norm(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, float *norm,
+                 void *workspace, int64_t workspace_bytes, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    return grads_common(count, grads, numel, dtypes, true, false, nullptr, norm, 0.0f, 0.0f, workspace,
+                        workspace_bytes, stream);
+}
+
+int s6_grad_clip(int64_t count, void *const *grads, const int64_t *numel, const int32_t *dtypes, const float *norm,
+                 float max_norm, float eps, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    return grads_common(count, grads, numel, dtypes, false, true, norm, nullptr, max_norm, eps, nullptr, 0, stream);
+}
+
+int s6_clip_grad_norm(int64_t count, void *const *grads, const int64_t *numel, const int32_t *dtypes, float max_norm,
+                      float eps, float *norm, void *workspace, int64_t workspace_bytes, s6_stream_t stream) {
+    DeviceRestore restore_device;
+    return grads_common(count, grads, numel, dtypes, true, true, nullptr, norm, max_norm, eps, workspace,
+                        workspace_bytes, stream);
+}
+
+}  // extern "C"
