@@ -15,6 +15,7 @@ Functions (same names as the C ABI):
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -480,34 +481,62 @@ def s6_block_step(x, conv_state, h_ssm, w, eps=1e-5, stream=None):
 
 # ------------------------------------------------- training-step operators
 # These pass a workspace that torch allocates on the stream of the call, so calls
-# on several streams, and several captured graphs, do not share one.
-_HERE_NOW = contextlib.nullcontext()
+# on several streams, and several captured graphs, do not share one.  At small
+# sizes the time of a call is the time of this code: it allocates little and looks
+# at each tensor once.
+_AS_IT_IS = contextlib.nullcontext()
 
 
-def _on(dev, stream):
+def _on(torch, dev, stream):
     """A context in which ``dev`` is the current device and ``stream`` (None: its
     current stream) the current stream, for the launch and for what is allocated."""
-    torch = _torch()
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    return _HERE_NOW if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _AS_IT_IS if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _workspace(need, where, dev):
+def _raw_stream(torch, dev):
+    """The current stream of ``dev`` as the C ABI takes it."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _arg(t, name, dtype, shape, dev):
+    """_ptr for a tensor that is as it should be; anything else is left to _ptr to name."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, name, dtype, shape, dev)
+
+
+def _workspace(torch, need, where, like):
     if need < 0:
         raise S6Error(need, where)
-    return _torch().empty(need, dtype=_torch().uint8, device=dev)
+    return like.new_empty(need, dtype=torch.uint8)
 
 
-def _cuda(t, name):
-    torch = _torch()
+def _cuda(torch, t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t
+
+
+def _norm_dims(torch, x, branch, eps, name):
+    """The sizes and types of a LayerNorm of x whose branch side is of type `branch`."""
+    if _cuda(torch, x, "x").dim() < 1:
+        raise ValueError("x must have a last dimension to normalise")
+    xc = _io_code(x)
+    if branch is not x.dtype and branch is not torch.bfloat16:
+        raise TypeError(f"{name} must be {x.dtype}, or bfloat16 beside a float32 x, got {branch}")
+    W = x.shape[-1]
+    return NormDims(x.numel() // W if W else 0, W, xc, xc if branch is x.dtype else S6_BF16, eps)
 
 
 def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtype=None, want_stats=True,
@@ -519,30 +548,28 @@ def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtyp
     Returns (y, s, mean, rstd): s is x when there is no r; mean and rstd [...] float32
     are for s6_layernorm_bwd (None unless want_stats)."""
     torch = _torch()
-    if _cuda(x, "x").dim() < 1:
-        raise ValueError("x must have a last dimension to normalise")
-    shape, W, dev = x.shape, x.shape[-1], x.device
     if y_dtype is None:
-        y_dtype = r.dtype if r is not None else y.dtype if y is not None else x.dtype
-    if y_dtype not in (x.dtype, torch.bfloat16):
-        raise TypeError(f"the branch type must be {x.dtype} or bfloat16 beside a {x.dtype} stream, got {y_dtype}")
+        t = r if r is not None else y if y is not None else x
+        y_dtype = _cuda(torch, t, "r, y or x").dtype
     if s is not None and r is None:
         raise ValueError("s is the sum x + r: it needs r")
-    f32 = torch.float32
-    xc = _io_code(x)
-    yc = xc if y_dtype == x.dtype else S6_BF16
-    with _on(dev, stream):
+    dims = _norm_dims(torch, x, y_dtype, float(eps), "the branch type")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    width = shape[-1:]
+    mean = rstd = None
+    with _on(torch, dev, stream):
         if y is None:
-            y = torch.empty(shape, dtype=y_dtype, device=dev)
+            y = x.new_empty(shape, dtype=y_dtype)
         if r is not None and s is None:
-            s = torch.empty_like(x)
-        stats = torch.empty((2,) + shape[:-1], dtype=f32, device=dev) if want_stats else (None, None)
-        mean, rstd = stats[0], stats[1]
-        dims = NormDims(x.numel() // W if W else 0, W, xc, yc, float(eps))
+            s = x.new_empty(shape)
+        if want_stats:
+            mean = x.new_empty(shape[:-1], dtype=f32)
+            rstd = torch.empty_like(mean)
         _check(lib().s6_layernorm_fwd(
-            ctypes.byref(dims), _ptr(x, "x"), _ptr(r, "r", y_dtype, shape, dev), _ptr(w, "w", f32, (W,), dev),
-            _ptr(b, "b", f32, (W,), dev), _ptr(s, "s", x.dtype, shape, dev), _ptr(y, "y", y_dtype, shape, dev),
-            _ptr(mean, "mean"), _ptr(rstd, "rstd"), _stream(None, dev)), "s6_layernorm_fwd")
+            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(r, "r", y_dtype, shape, dev),
+            _arg(w, "w", f32, width, dev), _arg(b, "b", f32, width, dev), _arg(s, "s", x.dtype, shape, dev),
+            _arg(y, "y", y_dtype, shape, dev), mean.data_ptr() if want_stats else None,
+            rstd.data_ptr() if want_stats else None, _raw_stream(torch, dev)), "s6_layernorm_fwd")
     return y, (x if r is None else s), mean, rstd
 
 
@@ -554,26 +581,24 @@ def s6_layernorm_bwd(dy, x, mean, rstd, w=None, ds=None, dx=None, want_params=Tr
     tensors: dx [..., W] (with respect to s, and so to x and r), dw and db [W] (None
     unless want_params)."""
     torch = _torch()
-    if _cuda(x, "x").dim() < 1:
-        raise ValueError("x must have a last dimension")
-    shape, W, dev = x.shape, x.shape[-1], x.device
-    if _cuda(dy, "dy").dtype not in (x.dtype, torch.bfloat16):
-        raise TypeError(f"dy must be {x.dtype} or bfloat16 beside a {x.dtype} stream, got {dy.dtype}")
-    f32 = torch.float32
-    xc = _io_code(x)
-    dims = NormDims(x.numel() // W if W else 0, W, xc, xc if dy.dtype == x.dtype else S6_BF16, 0.0)
+    dims = _norm_dims(torch, x, _cuda(torch, dy, "dy").dtype, 0.0, "dy")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    rows, width = shape[:-1], shape[-1:]
     L = lib()
-    with _on(dev, stream):
+    dw = db = None
+    with _on(torch, dev, stream):
         if dx is None:
-            dx = torch.empty(shape, dtype=f32, device=dev)
-        dw, db = torch.empty((2, W), dtype=f32, device=dev) if want_params else (None, None)
-        ws = _workspace(L.s6_layernorm_bwd_workspace(ctypes.byref(dims)), "s6_layernorm_bwd", dev)
-        rows = shape[:-1]
+            dx = x.new_empty(shape, dtype=f32)
+        if want_params:
+            dw = x.new_empty(width, dtype=f32)
+            db = torch.empty_like(dw)
+        ws = _workspace(torch, L.s6_layernorm_bwd_workspace(ctypes.byref(dims)), "s6_layernorm_bwd", x)
         _check(L.s6_layernorm_bwd(
-            ctypes.byref(dims), _ptr(x, "x"), _ptr(mean, "mean", f32, rows, dev), _ptr(rstd, "rstd", f32, rows, dev),
-            _ptr(w, "w", f32, (W,), dev), _ptr(dy, "dy", dy.dtype, shape, dev), _ptr(ds, "ds", f32, shape, dev),
-            _ptr(dx, "dx", f32, shape, dev), _ptr(dw, "dw"), _ptr(db, "db"), ws.data_ptr(), ws.numel(),
-            _stream(None, dev)), "s6_layernorm_bwd")
+            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(mean, "mean", f32, rows, dev),
+            _arg(rstd, "rstd", f32, rows, dev), _arg(w, "w", f32, width, dev), _arg(dy, "dy", dy.dtype, shape, dev),
+            _arg(ds, "ds", f32, shape, dev), _arg(dx, "dx", f32, shape, dev), dw.data_ptr() if want_params else None,
+            db.data_ptr() if want_params else None, ws.data_ptr(), ws.numel(), _raw_stream(torch, dev)),
+            "s6_layernorm_bwd")
     return {"dx": dx, "dw": dw, "db": db}
 
 
@@ -582,108 +607,100 @@ def causal_conv1d_silu_bwd(x, conv_w, dout, conv_b=None, stream=None):
     float32 (the du of s6_scan_bwd) or x's type.  Returns a dict of float32 tensors: dx
     [Bt, L, d], dconv_w [d, K], dconv_b [d] (None without conv_b)."""
     torch = _torch()
-    if _cuda(x, "x").dim() != 3:
+    if _cuda(torch, x, "x").dim() != 3:
         raise ValueError("x must be [batch, seqlen, d_inner]")
-    Bt, L, d = x.shape
-    K = _cuda(conv_w, "conv_w").shape[-1]
-    dev, f32 = x.device, torch.float32
-    if _cuda(dout, "dout").dtype not in (f32, x.dtype):
-        raise TypeError(f"dout must be float32 or {x.dtype}, got {dout.dtype}")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    Bt, L, d = shape
+    K = _cuda(torch, conv_w, "conv_w").shape[-1]
+    gt = _cuda(torch, dout, "dout").dtype
+    if gt is not f32 and gt is not x.dtype:
+        raise TypeError(f"dout must be float32 or {x.dtype}, got {gt}")
     dims = Dims(Bt, L, d, 1, K, _io_code(x))
     lb = lib()
-    with _on(dev, stream):
-        dx = torch.empty((Bt, L, d), dtype=f32, device=dev)
-        dw = torch.empty((d, K), dtype=f32, device=dev)
-        db = torch.empty((d,), dtype=f32, device=dev) if conv_b is not None else None
-        ws = _workspace(lb.causal_conv1d_silu_bwd_workspace(ctypes.byref(dims)), "causal_conv1d_silu_bwd", dev)
+    with _on(torch, dev, stream):
+        dx = x.new_empty(shape, dtype=f32)
+        dw = x.new_empty((d, K), dtype=f32)
+        db = x.new_empty((d,), dtype=f32) if conv_b is not None else None
+        ws = _workspace(torch, lb.causal_conv1d_silu_bwd_workspace(ctypes.byref(dims)), "causal_conv1d_silu_bwd", x)
         _check(lb.causal_conv1d_silu_bwd(
-            ctypes.byref(dims), _ptr(x, "x"), _ptr(conv_w, "conv_w", f32, (d, K), dev),
-            _ptr(conv_b, "conv_b", f32, (d,), dev), _ptr(dout, "dout", dout.dtype, (Bt, L, d), dev), _io_code(dout),
-            _ptr(dx, "dx"), _ptr(dw, "dconv_w"), _ptr(db, "dconv_b"), ws.data_ptr(), ws.numel(),
-            _stream(None, dev)), "causal_conv1d_silu_bwd")
+            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(conv_w, "conv_w", f32, (d, K), dev),
+            _arg(conv_b, "conv_b", f32, (d,), dev), _arg(dout, "dout", gt, shape, dev), _io_code(dout),
+            dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), ws.data_ptr(), ws.numel(),
+            _raw_stream(torch, dev)), "causal_conv1d_silu_bwd")
     return {"dx": dx, "dconv_w": dw, "dconv_b": db}
 
 
-class _GradList:
-    """The tensors of a call as the host arrays that the library reads."""
-
-    def __init__(self, grads, device=None):
-        torch = _torch()
-        if isinstance(grads, torch.Tensor):
-            grads = (grads,)
-        elif isinstance(grads, dict):
-            grads = grads.values()
-        ts = [g for g in grads if g is not None]
-        codes = {torch.float32: S6_F32, torch.bfloat16: S6_BF16}
-        dev = _cuda(ts[0], "grads[0]").device if ts else device
-        if ts and device is not None and dev != device:
-            raise ValueError(f"the gradients are on {dev}, norm on {device}")
+def _grad_list(torch, grads, norm):
+    """The tensors of a call as what the library reads, (count, and the addresses of the
+    host arrays of pointers, lengths and types), the arrays, and the tensors' device
+    (without tensors that of norm, or the current one)."""
+    T = torch.Tensor
+    if isinstance(grads, T):
+        grads = (grads,)
+    elif isinstance(grads, dict):
+        grads = grads.values()
+    ts = [g for g in grads if g is not None]
+    if norm is not None:
+        if not isinstance(norm, T) or norm.dtype is not torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be a float32 tensor of 1 element")
+        _ptr(norm, "norm")
+        dev = norm.device
+    elif ts:
+        dev = _cuda(torch, ts[0], "grads[0]").device
+    else:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    codes = {torch.float32: S6_F32, torch.bfloat16: S6_BF16}
+    try:  # three passes in C over a list that is as it should be
+        good = all(map(T.is_contiguous, ts)) and set(map(T.get_device, ts)) <= {dev.index}
+        types = array.array("i", [codes[t.dtype] for t in ts])
+    except (TypeError, KeyError):
+        good = False
+    if not good:
         for i, t in enumerate(ts):
-            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev and t.is_contiguous()):
-                _ptr(t, f"grads[{i}]", device=dev)  # raises what is wrong
-            if t.dtype not in codes:
-                raise TypeError(f"grads[{i}] must be float32 or bfloat16, got {t.dtype}")
-        n = len(ts)
-        self.device, self.count = dev, n
-        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
-        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in ts])
-        self.codes = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in ts])
-
-
-def _norm_out(norm, dev):
-    torch = _torch()
-    if norm is None:
-        return torch.empty((), dtype=torch.float32, device=dev)
-    _ptr(norm, "norm", torch.float32, None, dev)
-    if norm.numel() != 1:
-        raise ValueError(f"norm has {norm.numel()} elements, expected 1")
-    return norm
-
-
-def _norm_device(norm, dev):
-    if dev is not None:
-        return dev
-    torch = _torch()
-    return norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
+            _ptr(t, f"grads[{i}]", device=dev)  # says what is wrong
+        raise TypeError(f"gradients must be float32 or bfloat16, got {sorted({str(t.dtype) for t in ts})}")
+    kept = array.array("q", map(T.data_ptr, ts)), array.array("q", map(T.numel, ts)), types
+    return (len(ts),) + tuple(a.buffer_info()[0] for a in kept), kept, dev
 
 
 def s6_grad_norm(grads, norm=None, stream=None):
     """The norm of all gradients taken as one vector: a float32 scalar on the device.
     grads: tensors (a list, or the dict of a backward call; None entries are left out),
     float32 or bfloat16, contiguous, on one device.  norm: where to put it."""
-    g = _GradList(grads, norm.device if norm is not None else None)
-    dev = _norm_device(norm, g.device)
+    torch = _torch()
+    g, kept, dev = _grad_list(torch, grads, norm)
     L = lib()
-    with _on(dev, stream):
-        norm = _norm_out(norm, dev)
-        ws = _workspace(L.s6_grad_workspace(g.count, g.numel), "s6_grad_norm", dev)
-        _check(L.s6_grad_norm(g.count, g.ptrs, g.numel, g.codes, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                              _stream(None, dev)), "s6_grad_norm")
+    with _on(torch, dev, stream):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = _workspace(torch, L.s6_grad_workspace(g[0], g[2]), "s6_grad_norm", norm)
+        _check(L.s6_grad_norm(*g, norm.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(torch, dev)),
+               "s6_grad_norm")
     return norm
 
 
 def s6_grad_clip(grads, norm, max_norm, eps=1e-6, stream=None):
     """Scales the gradients in place by min(1, max_norm / (norm + eps)), for a norm that is
     on the device already (one that ranks have combined, say).  No two tensors may overlap."""
-    g = _GradList(grads, _cuda(norm, "norm").device)
-    dev = norm.device
-    with _on(dev, stream):
-        norm = _norm_out(norm, dev)
-        _check(lib().s6_grad_clip(g.count, g.ptrs, g.numel, g.codes, norm.data_ptr(), float(max_norm), float(eps),
-                                  _stream(None, dev)), "s6_grad_clip")
+    torch = _torch()
+    g, kept, dev = _grad_list(torch, grads, _cuda(torch, norm, "norm"))
+    with _on(torch, dev, stream):
+        _check(lib().s6_grad_clip(*g, norm.data_ptr(), float(max_norm), float(eps), _raw_stream(torch, dev)),
+               "s6_grad_clip")
 
 
 def s6_clip_grad_norm(grads, max_norm, eps=1e-6, norm=None, stream=None):
     """s6_grad_norm and s6_grad_clip in one call: scales the gradients in place by
     min(1, max_norm / (norm + eps)) and returns norm, as it was before."""
-    g = _GradList(grads, norm.device if norm is not None else None)
-    dev = _norm_device(norm, g.device)
+    torch = _torch()
+    g, kept, dev = _grad_list(torch, grads, norm)
     L = lib()
-    with _on(dev, stream):
-        norm = _norm_out(norm, dev)
-        ws = _workspace(L.s6_grad_workspace(g.count, g.numel), "s6_clip_grad_norm", dev)
-        _check(L.s6_clip_grad_norm(g.count, g.ptrs, g.numel, g.codes, float(max_norm), float(eps), norm.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), _stream(None, dev)), "s6_clip_grad_norm")
+    with _on(torch, dev, stream):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = _workspace(torch, L.s6_grad_workspace(g[0], g[2]), "s6_clip_grad_norm", norm)
+        _check(L.s6_clip_grad_norm(*g, float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   _raw_stream(torch, dev)), "s6_clip_grad_norm")
     return norm
 
 

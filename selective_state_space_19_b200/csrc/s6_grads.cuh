@@ -4,8 +4,8 @@
 //     n = sqrt(sum over all tensors and elements of g^2)
 //     c = min(1, max_norm / (n + eps)),   g <- c g  where c < 1
 //
-// A list of tensors is cut into chunks of kGradChunk elements of one tensor
-// each; blocks walk the chunks with a fixed stride, so small and large tensors
+// A list of tensors is cut into chunks of kGradChunkSmall or -Large elements of
+// one tensor each; blocks walk the chunks with a fixed stride, so small and large tensors
 // balance and the order of all additions is fixed.  Pointers and lengths travel
 // in the kernel's parameters: nothing is copied to the device beforehand, and a
 // captured graph holds its own table.
@@ -25,9 +25,9 @@
 
 namespace s6 {
 
-constexpr int kGradChunk = 8192;
+constexpr int kGradChunkSmall = 4096, kGradChunkLarge = 16384;
 constexpr int kGradThreads = 256;
-constexpr int kGradMaxBlocks = 148 * 4;
+constexpr int kGradMaxBlocks = 148 * 6;
 constexpr int kGradTensors = 1024;  // of one launch; the table is 17 KB of parameters
 constexpr int kGradFew = 96;        // a table for short lists
 
@@ -36,7 +36,7 @@ struct GradTable {
     void *ptr[M];       // bit 0 set: bfloat16
     long long n[M];     // elements
     int end[M];         // chunks of the tensors up to and with this one
-    int tensors, chunks;
+    int tensors, chunks, chunk;  // chunk: elements of one
 };
 
 struct GradScaleArgs {
@@ -63,12 +63,12 @@ __device__ __forceinline__ GradSpan grad_span(const GradTable<M> &t, int chunk) 
         else
             lo = mid + 1;
     }
-    const long long at = static_cast<long long>(chunk - (lo ? t.end[lo - 1] : 0)) * kGradChunk;
+    const long long at = static_cast<long long>(chunk - (lo ? t.end[lo - 1] : 0)) * t.chunk;
     const uintptr_t raw = reinterpret_cast<uintptr_t>(t.ptr[lo]);
     GradSpan s;
     s.bf16 = raw & 1u;
     s.p = reinterpret_cast<void *>((raw & ~static_cast<uintptr_t>(1)) + at * (s.bf16 ? 2 : 4));
-    s.n = static_cast<int>(t.n[lo] - at < kGradChunk ? t.n[lo] - at : kGradChunk);
+    s.n = static_cast<int>(t.n[lo] - at < t.chunk ? t.n[lo] - at : t.chunk);
     return s;
 }
 
@@ -185,7 +185,7 @@ __device__ __forceinline__ double grad_block_sum(double v, double *sh) {
 }
 
 template <int M>
-__global__ void __launch_bounds__(kGradThreads) s6_grad_square_kernel(const __grid_constant__ GradTable<M> t,
+__global__ void __launch_bounds__(kGradThreads, 6) s6_grad_square_kernel(const __grid_constant__ GradTable<M> t,
                                                                      double *part) {
     __shared__ double sh[kGradThreads / 32];
     cudaTriggerProgrammaticLaunchCompletion();
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kGradThreads) s6_grad_square_kernel(const __gr
 }
 
 template <int M>
-__global__ void __launch_bounds__(kGradThreads) s6_grad_scale_kernel(const __grid_constant__ GradTable<M> t,
+__global__ void __launch_bounds__(kGradThreads, 6) s6_grad_scale_kernel(const __grid_constant__ GradTable<M> t,
                                                                     const GradScaleArgs a) {
     __shared__ double sh[kGradThreads / 32];
     cudaGridDependencySynchronize();

@@ -15,20 +15,38 @@
 //
 // Both are bound by HBM: a row is read once into registers, in the storage
 // type, and everything is computed in float32 from there.  A row belongs to
-// one warp up to kNormPerWarp elements and to one block above that; the warp
+// one warp up to kNormWarpWidth elements and to one block above that; the warp
 // or block walks rows with a fixed stride and fetches the next row while it
-// reduces the present one.  Wider rows than kNormMaxWarps warps hold take the
-// _wide kernels, which read a row more than once.
+// reduces the present one.  Rows above kNormMaxWidth take the _wide kernels,
+// which read a row more than once.
 #pragma once
 
 #include "s6_vec.cuh"
 
 namespace s6 {
 
-constexpr int kNormPerWarp = 512;   // elements of a row that one warp holds
-constexpr int kNormMaxWarps = 16;   // warps that share a row
-constexpr int kNormMaxWidth = kNormPerWarp * kNormMaxWarps;
-constexpr int kNormBlockWarps = 8;  // rows in flight in a block of one-warp rows
+constexpr int kNormWarpWidth = 512;   // widest row of one warp: 16 elements a lane
+constexpr int kNormBlockWarps = 4;    // warps (rows in flight) of a block of one-warp rows
+constexpr int kNormMaxWidth = 8192;   // widest row held in registers
+constexpr int kNormMaxWarps = 32;     // warps that share a row, at most
+
+// Elements of a row that a thread holds where several warps share it.  The
+// backward, which also holds sums for each of its columns, takes 16 above 4096
+// (fewer, larger threads: a block's registers are bounded).
+constexpr int norm_block_elems(int64_t width, bool bwd) { return bwd && width > 4096 ? 16 : 8; }
+// Warps resident on an SM, by the elements that a thread holds: what the
+// registers allow (the launch bounds below hold the compiler to it).
+constexpr int norm_warps_resident(int elems, bool one_warp, bool bwd) {
+    return one_warp ? (bwd ? (elems <= 4 ? 24 : elems <= 8 ? 20 : elems <= 12 ? 16 : 12)
+                           : (elems <= 4 ? 32 : elems <= 8 ? 28 : elems <= 12 ? 20 : 16))
+                    : (bwd ? (elems <= 8 ? 21 : 16) : 32);
+}
+constexpr int norm_max_threads(int elems, bool one_warp, bool bwd) {
+    return one_warp ? 32 * kNormBlockWarps : 32 * norm_warps_resident(elems, false, bwd);
+}
+constexpr int norm_min_blocks(int elems, bool one_warp, bool bwd) {
+    return one_warp ? norm_warps_resident(elems, true, bwd) / kNormBlockWarps : 1;
+}
 
 struct NormFwdArgs {
     long long rows;
@@ -52,7 +70,8 @@ struct NormBwdArgs {
 };
 
 // The sum of v over the threads of a row: a warp's, or a block's through `red`
-// (one slot a warp).  Every thread adds the slots in the same order.
+// (one slot a warp; the slots behind the block's own warps are zero).  Every
+// thread adds the slots in the same order.
 template <bool WARP>
 __device__ __forceinline__ float row_sum(float v, float *red, int nwarps) {
     v = warp_sum(v);
@@ -61,18 +80,29 @@ __device__ __forceinline__ float row_sum(float v, float *red, int nwarps) {
             red[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.0f;
-        for (int i = 0; i < nwarps; ++i)
-            v += red[i];
+        for (int i = 0; i < nwarps; i += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(red + i);
+            v += (t.x + t.y) + (t.z + t.w);
+        }
     }
     return v;
 }
 
+// Zeroes `n` slots; the first barrier of row_sum's caller comes after it.
+__device__ __forceinline__ void clear_slots(float *red, int n) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        red[i] = 0.0f;
+    __syncthreads();
+}
+
 template <typename X, typename Y, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
+__global__ void __launch_bounds__(norm_max_threads(NV *V, WARP, false), norm_min_blocks(NV *V, WARP, false))
     s6_layernorm_fwd_kernel(const NormFwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ float red[2][kNormMaxWarps];
+    __shared__ __align__(16) float red[2][kNormMaxWarps];
+    if constexpr (!WARP)
+        clear_slots(red[0], 2 * kNormMaxWarps);
     const int nwarps = blockDim.x >> 5;
     const int G = WARP ? 32 : blockDim.x;                     // threads of a row
     const int li = WARP ? (threadIdx.x & 31) : threadIdx.x;  // this thread among them
@@ -97,23 +127,26 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
     long long row = per * blockIdx.x + (WARP ? (threadIdx.x >> 5) : 0);
     typename VX::raw xr[NV];
     typename VY::raw rr[NV];
+    const int c0 = li * V, dc = G * V;  // this thread's first column, and from one to the next
     auto fetch = [&](long long at) {
+        const X *xp = x + at * W + c0;
+        const Y *rp = r + at * W + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + li) * V;
-            const bool in = c < W;
-            xr[j] = in ? VX::load(x + at * W + c) : VX::zero();
+            const bool in = c0 + j * dc < W;
+            xr[j] = in ? VX::load(xp + j * dc) : VX::zero();
             if (r)
-                rr[j] = in ? VY::load(r + at * W + c) : VY::zero();
+                rr[j] = in ? VY::load(rp + j * dc) : VY::zero();
         }
     };
     if (row < a.rows)
         fetch(row);
     for (; row < a.rows; row += step) {
         float v[NV][V], sum = 0.0f;
+        X *sp = s + row * W + c0;
+        Y *yp = y + row * W + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + li) * V;
             VX::unpack(xr[j], v[j]);
             if (r) {
                 float t[V];
@@ -121,8 +154,8 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     v[j][i] += t[i];
-                if (s && c < W)
-                    VX::store(s + row * W + c, VX::pack(v[j]));
+                if (s && c0 + j * dc < W)
+                    VX::store(sp + j * dc, VX::pack(v[j]));
             }
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -136,7 +169,7 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
         float sq = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if ((j * G + li) * V < W) {
+            if (c0 + j * dc < W) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     v[j][i] -= mean;
@@ -152,13 +185,12 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + li) * V;
-            if (c < W) {
+            if (c0 + j * dc < W) {
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     o[i] = fmaf(v[j][i] * rstd, wv[j][i], bv[j][i]);
-                VY::store(y + row * W + c, VY::pack(o));
+                VY::store(yp + j * dc, VY::pack(o));
             }
         }
     }
@@ -173,7 +205,7 @@ template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel(const NormFwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ float red[2][kNormMaxWarps];
+    __shared__ __align__(16) float red[2][kNormMaxWarps];
     const int W = a.width;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X *x = static_cast<const X *>(a.x) + row * W;
@@ -229,12 +261,14 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
 // its registers until the block's last row; the block then writes one row of
 // partial sums and s6_sum_parts_kernel adds those up.
 template <typename X, typename Y, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
+__global__ void __launch_bounds__(norm_max_threads(NV *V, WARP, true), norm_min_blocks(NV *V, WARP, true))
     s6_layernorm_bwd_kernel(const NormBwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
     using VF = IoVec<float, V>;
-    __shared__ float red[2][2][kNormMaxWarps];
+    __shared__ __align__(16) float red[2][2][kNormMaxWarps];
+    if constexpr (!WARP)
+        clear_slots(red[0][0], 4 * kNormMaxWarps);
     const int nwarps = blockDim.x >> 5;
     const int G = WARP ? 32 : blockDim.x;
     const int li = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -259,14 +293,17 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
     typename VX::raw xr[NV];
     typename VY::raw gr[NV];
     float mean = 0.0f, rstd = 0.0f;
+    const int c0 = li * V, dc = G * V;
     auto fetch = [&](long long at) {
         mean = a.mean[at];
         rstd = a.rstd[at];
+        const X *xp = x + at * W + c0;
+        const Y *gp = dy + at * W + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + li) * V;
-            xr[j] = c < W ? VX::load(x + at * W + c) : VX::zero();
-            gr[j] = c < W ? VY::load(dy + at * W + c) : VY::zero();
+            const bool in = c0 + j * dc < W;
+            xr[j] = in ? VX::load(xp + j * dc) : VX::zero();
+            gr[j] = in ? VY::load(gp + j * dc) : VY::zero();
         }
     };
     if (row < a.rows)
@@ -279,7 +316,7 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
         for (int j = 0; j < NV; ++j) {
             VX::unpack(xr[j], h[j]);
             VY::unpack(gr[j], g[j]);
-            if ((j * G + li) * V < W) {
+            if (c0 + j * dc < W) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     h[j][i] = (h[j][i] - mean) * q;
@@ -293,13 +330,13 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
         }
         if (row + step < a.rows)
             fetch(row + step);
+        const float *dsp = a.ds + row * W + c0;
+        float *dxp = a.dx + row * W + c0;
         typename VF::raw dsr[NV];
         if (a.ds) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * G + li) * V;
-                dsr[j] = c < W ? VF::load(a.ds + row * W + c) : VF::zero();
-            }
+            for (int j = 0; j < NV; ++j)
+                dsr[j] = c0 + j * dc < W ? VF::load(dsp + j * dc) : VF::zero();
         }
         s0 = warp_sum(s0);
         s1 = warp_sum(s1);
@@ -314,20 +351,21 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
             }
             __syncthreads();
             s0 = s1 = 0.0f;
-            for (int i = 0; i < nwarps; ++i) {
-                s0 += slot[0][i];
-                s1 += slot[1][i];
+            for (int i = 0; i < nwarps; i += 4) {
+                const float4 t0 = *reinterpret_cast<const float4 *>(slot[0] + i);
+                const float4 t1 = *reinterpret_cast<const float4 *>(slot[1] + i);
+                s0 += (t0.x + t0.y) + (t0.z + t0.w);
+                s1 += (t1.x + t1.y) + (t1.z + t1.w);
             }
         }
-        const float c0 = s0 * a.inv_w, c1 = s1 * a.inv_w;
+        const float m0 = s0 * a.inv_w, m1 = s1 * a.inv_w;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + li) * V;
-            if (c < W) {
+            if (c0 + j * dc < W) {
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    o[i] = q * (g[j][i] - fmaf(h[j][i], c1, c0));
+                    o[i] = q * (g[j][i] - fmaf(h[j][i], m1, m0));
                 if (a.ds) {
                     float t[V];
                     VF::unpack(dsr[j], t);
@@ -335,7 +373,7 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
                     for (int i = 0; i < V; ++i)
                         o[i] += t[i];
                 }
-                VF::store(a.dx + row * W + c, VF::pack(o));
+                VF::store(dxp + j * dc, VF::pack(o));
             }
         }
     }
@@ -345,7 +383,7 @@ __global__ void __launch_bounds__(32 * (WARP ? kNormBlockWarps : kNormMaxWarps))
     float *part = a.part + static_cast<long long>(blockIdx.x) * 2 * W;
     if constexpr (WARP) {
         // the block's warps hold sums of the same columns: add them up in order
-        __shared__ float sums[2][kNormPerWarp];
+        __shared__ float sums[2][kNormWarpWidth];
         for (int k = 0; k < nwarps; ++k) {
             if ((threadIdx.x >> 5) == k) {
 #pragma unroll
@@ -383,7 +421,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_k
                                                                                     float2 *sums) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ float red[2][kNormMaxWarps];
+    __shared__ __align__(16) float red[2][kNormMaxWarps];
     const int W = a.width;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X *x = static_cast<const X *>(a.x) + row * W;

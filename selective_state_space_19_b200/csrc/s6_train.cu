@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include "s6.h"
 #include "s6_common.cuh"
@@ -81,27 +82,30 @@ int check_norm_dims(const s6_norm_dims *dims) {
 }
 
 struct NormPlan {
-    int warps;      // warps that share a row; 1: a row a warp, kNormBlockWarps rows a block
+    int warps;  // warps that share a row; 1: a row a warp, kNormBlockWarps rows a block
+    int elems;  // elements of a row that a thread holds, at most
     int threads;
     int64_t blocks;
 };
 
-// One warp a row up to 512 elements, above that as many warps as hold the row at
-// 16 elements a thread.  About `resident` warps for each SM, which walk the rows.
-NormPlan norm_plan(int64_t rows, int64_t width, int resident) {
+// One warp a row up to kNormWarpWidth elements, above that as many warps as hold the
+// row; as many blocks as are resident, which walk the rows.
+NormPlan norm_plan(int64_t rows, int64_t width, bool bwd) {
     NormPlan p;
-    p.warps = static_cast<int>(ceil_div(width, s6::kNormPerWarp));
-    if (p.warps == 1) {
+    if (width <= s6::kNormWarpWidth) {
+        p.warps = 1;
+        p.elems = static_cast<int>(4 * ceil_div(width, 128));
         p.threads = 32 * s6::kNormBlockWarps;
-        p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps), kSMs * resident / s6::kNormBlockWarps);
+        p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps),
+                            kSMs * s6::norm_warps_resident(p.elems, true, bwd) / s6::kNormBlockWarps);
     } else {
+        p.elems = s6::norm_block_elems(width, bwd);
+        p.warps = static_cast<int>(ceil_div(width, 32 * p.elems));
         p.threads = 32 * p.warps;
-        p.blocks = std::min(rows, kSMs * std::max<int64_t>(1, resident / p.warps));
+        p.blocks = std::min(rows, kSMs * (s6::norm_warps_resident(p.elems, false, bwd) / p.warps));
     }
     return p;
 }
-
-constexpr int kNormFwdResident = 32, kNormBwdResident = 16;
 
 // Runs of rows of the wide backward's second kernel: enough blocks to fill the
 // SMs at its 128-thread blocks, whatever the vector width.
@@ -110,24 +114,34 @@ int64_t norm_wide_runs(int64_t rows, int64_t width) {
     return std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
 }
 
-template <typename X, typename Y, int V, int NV>
-int norm_fwd_nv(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(p.blocks));
-    if (p.warps == 1)
-        s6::s6_layernorm_fwd_kernel<X, Y, V, NV, true><<<grid, p.threads, 0, st>>>(a);
-    else
-        s6::s6_layernorm_fwd_kernel<X, Y, V, NV, false><<<grid, p.threads, 0, st>>>(a);
+template <typename X, typename Y, int V, int NV, bool WARP>
+int norm_launch(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    s6::s6_layernorm_fwd_kernel<X, Y, V, NV, WARP><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
     return launch_status(cudaGetLastError());
 }
 
-template <typename X, typename Y, int V, int NV>
-int norm_bwd_nv(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(p.blocks));
-    if (p.warps == 1)
-        s6::s6_layernorm_bwd_kernel<X, Y, V, NV, true><<<grid, p.threads, 0, st>>>(a);
-    else
-        s6::s6_layernorm_bwd_kernel<X, Y, V, NV, false><<<grid, p.threads, 0, st>>>(a);
+template <typename X, typename Y, int V, int NV, bool WARP>
+int norm_launch(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    s6::s6_layernorm_bwd_kernel<X, Y, V, NV, WARP><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
     return launch_status(cudaGetLastError());
+}
+
+// The instantiation that holds p.elems elements a thread, as vectors of V.
+template <typename X, typename Y, int V, typename Args>
+int norm_dispatch(const Args &a, const NormPlan &p, cudaStream_t st) {
+    if (p.warps == 1) {
+        if (p.elems <= 4)
+            return norm_launch<X, Y, V, 4 / V, true>(a, p, st);
+        if (p.elems <= 8)
+            return norm_launch<X, Y, V, 8 / V, true>(a, p, st);
+        if (p.elems <= 12)
+            return norm_launch<X, Y, V, 12 / V, true>(a, p, st);
+        return norm_launch<X, Y, V, 16 / V, true>(a, p, st);
+    }
+    if constexpr (std::is_same<Args, s6::NormBwdArgs>::value)
+        if (p.elems > 8)
+            return norm_launch<X, Y, V, 16 / V, false>(a, p, st);
+    return norm_launch<X, Y, V, 8 / V, false>(a, p, st);
 }
 
 template <typename X, typename Y, int V>
@@ -138,23 +152,7 @@ int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
             <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a);
         return launch_status(cudaGetLastError());
     }
-    const NormPlan p = norm_plan(a.rows, a.width, kNormFwdResident);
-    const int64_t nv = ceil_div(a.width, V * 32 * p.warps);
-    if constexpr (V == 4) {
-        if (nv == 1)
-            return norm_fwd_nv<X, Y, 4, 1>(a, p, st);
-        if (nv == 2)
-            return norm_fwd_nv<X, Y, 4, 2>(a, p, st);
-        if (nv == 3)
-            return norm_fwd_nv<X, Y, 4, 3>(a, p, st);
-        return norm_fwd_nv<X, Y, 4, 4>(a, p, st);
-    } else {
-        if (nv <= 4)
-            return norm_fwd_nv<X, Y, 1, 4>(a, p, st);
-        if (nv <= 8)
-            return norm_fwd_nv<X, Y, 1, 8>(a, p, st);
-        return norm_fwd_nv<X, Y, 1, 16>(a, p, st);
-    }
+    return norm_dispatch<X, Y, V>(a, norm_plan(a.rows, a.width, false), st);
 }
 
 template <typename X, typename Y, int V>
@@ -175,20 +173,10 @@ int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db,
                         static_cast<unsigned>(parts));
         s6::s6_layernorm_bwd_wide_cols_kernel<X, Y, V><<<grid, s6::kNormColThreads, 0, st>>>(a, sums);
     } else {
-        const NormPlan p = norm_plan(a.rows, a.width, kNormBwdResident);
-        const int64_t nv = ceil_div(a.width, V * 32 * p.warps);
+        const NormPlan p = norm_plan(a.rows, a.width, true);
         parts = p.blocks;
         a.part = params ? part : nullptr;
-        int rc;
-        if constexpr (V == 4)
-            rc = nv == 1   ? norm_bwd_nv<X, Y, 4, 1>(a, p, st)
-                 : nv == 2 ? norm_bwd_nv<X, Y, 4, 2>(a, p, st)
-                 : nv == 3 ? norm_bwd_nv<X, Y, 4, 3>(a, p, st)
-                           : norm_bwd_nv<X, Y, 4, 4>(a, p, st);
-        else
-            rc = nv <= 4   ? norm_bwd_nv<X, Y, 1, 4>(a, p, st)
-                 : nv <= 8 ? norm_bwd_nv<X, Y, 1, 8>(a, p, st)
-                           : norm_bwd_nv<X, Y, 1, 16>(a, p, st);
+        const int rc = norm_dispatch<X, Y, V>(a, p, st);
         if (rc != S6_OK)
             return rc;
     }
@@ -213,7 +201,7 @@ struct ConvBwdPlan {
     int64_t tiles, blocks_y, run, runs;
 };
 
-constexpr int64_t kConvBwdBlocks = kSMs * 4;  // resident blocks of 4 warps
+constexpr int64_t kConvBwdBlocks = kSMs * s6::kConvBwdPerSM;
 constexpr int64_t kConvBwdMinRun = 16;        // tokens; shorter runs read more rows twice than they save
 
 int64_t conv_bwd_blocks_y(int64_t d, int64_t channels) {
@@ -277,7 +265,16 @@ int check_conv_bwd_dims(const s6_dims *dims) {
 }
 
 // --------------------------------------------------------------- gradients
-constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^24 chunks of one tensor
+constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^25 of the smaller chunks
+
+// Elements of a chunk: the larger size where even that gives every resident block
+// one, the smaller where the larger would leave SMs without work.
+int grad_chunk(int64_t count, const int64_t *numel) {
+    int64_t total = 0;
+    for (int64_t i = 0; i < count && total < kGradMaxNumel; ++i)
+        total += numel[i];
+    return total >= int64_t(s6::kGradMaxBlocks) * s6::kGradChunkLarge ? s6::kGradChunkLarge : s6::kGradChunkSmall;
+}
 
 // Checks a list; `write`: the tensors are written, so no two may share memory.
 int check_grads(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, bool write) {
@@ -324,10 +321,11 @@ template <int M, typename Fn>
 int for_tables(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, Fn fn) {
     s6::GradTable<M> t;
     t.tensors = t.chunks = 0;
+    t.chunk = grad_chunk(count, numel);
     for (int64_t i = 0; i < count; ++i) {
         if (numel[i] == 0)
             continue;
-        const int chunks = static_cast<int>(ceil_div(numel[i], s6::kGradChunk));  // at most 2^24 (check_grads)
+        const int chunks = static_cast<int>(ceil_div(numel[i], t.chunk));  // at most 2^25 (check_grads)
         if (t.tensors == M || t.chunks + chunks > (1 << 30)) {
             const int rc = fn(t);
             if (rc != S6_OK)
@@ -462,7 +460,7 @@ int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims) {
     const int64_t row = 2 * dims->width * static_cast<int64_t>(sizeof(float));
     if (dims->width > s6::kNormMaxWidth)
         return dims->rows * static_cast<int64_t>(sizeof(float2)) + norm_wide_runs(dims->rows, dims->width) * row;
-    return norm_plan(dims->rows, dims->width, kNormBwdResident).blocks * row;
+    return norm_plan(dims->rows, dims->width, true).blocks * row;
 }
 
 int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd, const float *w,
@@ -581,7 +579,7 @@ int64_t s6_grad_workspace(int64_t count, const int64_t *numel) {
             return S6_ERR_INVALID_ARG;
         if (numel[i] > kGradMaxNumel)
             return S6_ERR_UNSUPPORTED;
-        chunks += ceil_div(numel[i], s6::kGradChunk);
+        chunks += ceil_div(numel[i], s6::kGradChunkSmall);
     }
     const int64_t launches = count / (count <= s6::kGradFew ? s6::kGradFew : s6::kGradTensors) + 1 + (chunks >> 29);
     return launches * s6::kGradMaxBlocks * static_cast<int64_t>(sizeof(double));

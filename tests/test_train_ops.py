@@ -433,7 +433,7 @@ def test_gradient_lists_of_every_kind():
         S.s6_grad_norm([g["du"].t()])
     with pytest.raises(TypeError):
         S.s6_grad_norm([g["du"].half()])
-    with pytest.raises(ValueError, match="elements"):
+    with pytest.raises(ValueError, match="1 element"):
         S.s6_grad_norm(g, norm=torch.zeros(2, device="cuda"))
 
 
