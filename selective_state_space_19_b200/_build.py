@@ -68,24 +68,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
-    tag = ".tmp%d" % os.getpid()
+    tag = ".tmp%d.o" % os.getpid()
     jobs, objects = [], []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
         obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
         objects.append(obj)
         if not force and _fresh(obj, _needs(src)):
             continue
-        cmd = [_nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-c", "-o", obj + tag, src]
+        cmd = [_nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-c", "-o", obj[:-2] + tag, src]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), file=sys.stderr)
         jobs.append((subprocess.Popen(cmd), obj, cmd))
     failed = [cmd for p, _, cmd in jobs if p.wait() != 0]
     if failed:
+        for _, obj, _ in jobs:
+            if os.path.exists(obj[:-2] + tag):
+                os.remove(obj[:-2] + tag)
         raise subprocess.CalledProcessError(1, failed[0])
     for _, obj, _ in jobs:
-        os.replace(obj + tag, obj)
-    subprocess.check_call([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB + tag, *objects])
+        os.replace(obj[:-2] + tag, obj)
+    subprocess.check_call([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB + tag, *objects])  # (*.o is ignored by git)
     os.replace(LIB + tag, LIB)
     return LIB
 

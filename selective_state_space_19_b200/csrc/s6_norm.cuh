@@ -13,39 +13,41 @@
 //     dx = ds + q (g - sum(g)/W - h sum(g h)/W)        ds: the gradient that
 //     dw = sum over rows of dy h,  db = of dy          reaches s past the norm
 //
-// Both are bound by HBM: a row is read once into registers, in the storage
-// type, and everything is computed in float32 from there.  A row belongs to
-// one warp up to kNormWarpWidth elements and to one block above that; the warp
-// or block walks rows with a fixed stride and fetches the next row while it
-// reduces the present one.  Rows above kNormMaxWidth take the _wide kernels,
-// which read a row more than once.
+// Both are bound by HBM: a row is read once, in the storage type, and
+// everything is computed in float32 from there.  Three forms, by the width:
+//
+//  * up to kNormWarpWidth: a row is one warp's, in its registers.  The warp
+//    walks rows with a fixed stride and fetches the next one while it reduces
+//    the present one.
+//  * up to kNormMaxWidth: rows pass through shared memory, copied ahead of
+//    their use without registers.  Forward, a row is one warp's still, so it
+//    needs no barrier; backward, a block takes some rows at a time, a few
+//    warps sum each row, and then each thread does its own columns of all of
+//    them.  (Rows split over a block's registers, which this replaces, spent
+//    44 instructions an element on reductions and addresses at a width of 2560.)
+//  * above that: the _wide kernels, which read a row more than once.
+//
+// Vectors of 4 elements where the rows begin on one, else single elements:
+// rows of an odd width start anywhere, so the copies into shared memory are
+// made of 16-byte pieces that are aligned in global memory and keep the row's
+// place in them.
 #pragma once
+
+#include <type_traits>
 
 #include "s6_vec.cuh"
 
 namespace s6 {
 
-constexpr int kNormWarpWidth = 512;   // widest row of one warp: 16 elements a lane
-constexpr int kNormBlockWarps = 4;    // warps (rows in flight) of a block of one-warp rows
-constexpr int kNormMaxWidth = 8192;   // widest row held in registers
-constexpr int kNormMaxWarps = 32;     // warps that share a row, at most
+constexpr int kNormWarpWidth = 512;  // widest row of one warp's registers: 16 elements a lane
+constexpr int kNormBlockWarps = 4;   // warps (rows in flight) of a block of such rows
+constexpr int kNormMaxWidth = 8192;  // widest row that passes through shared memory
 
-// Elements of a row that a thread holds where several warps share it.  The
-// backward, which also holds sums for each of its columns, takes 16 above 4096
-// (fewer, larger threads: a block's registers are bounded).
-constexpr int norm_block_elems(int64_t width, bool bwd) { return bwd && width > 4096 ? 16 : 8; }
-// Warps resident on an SM, by the elements that a thread holds: what the
-// registers allow (the launch bounds below hold the compiler to it).
-constexpr int norm_warps_resident(int elems, bool one_warp, bool bwd) {
-    return one_warp ? (bwd ? (elems <= 4 ? 24 : elems <= 8 ? 20 : elems <= 12 ? 16 : 12)
-                           : (elems <= 4 ? 32 : elems <= 8 ? 28 : elems <= 12 ? 20 : 16))
-                    : (bwd ? (elems <= 8 ? 21 : 16) : 32);
-}
-constexpr int norm_max_threads(int elems, bool one_warp, bool bwd) {
-    return one_warp ? 32 * kNormBlockWarps : 32 * norm_warps_resident(elems, false, bwd);
-}
-constexpr int norm_min_blocks(int elems, bool one_warp, bool bwd) {
-    return one_warp ? norm_warps_resident(elems, true, bwd) / kNormBlockWarps : 1;
+// Warps of one-warp rows resident on an SM, by the elements that a lane holds:
+// what the registers allow (the launch bounds hold the compiler to it).
+__host__ __device__ constexpr int norm_warps_resident(int elems, bool bwd) {
+    return bwd ? (elems <= 4 ? 24 : elems <= 8 ? 20 : elems <= 12 ? 16 : 12)
+               : (elems <= 4 ? 32 : elems <= 8 ? 28 : elems <= 12 ? 20 : 16);
 }
 
 struct NormFwdArgs {
@@ -69,143 +71,123 @@ struct NormBwdArgs {
     float *part;  // [blocks][2][width]: the block's dw and db; null = neither is wanted
 };
 
-// The sum of v over the threads of a row: a warp's, or a block's through `red`
-// (one slot a warp; the slots behind the block's own warps are zero).  Every
-// thread adds the slots in the same order.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float *red, int nwarps) {
-    v = warp_sum(v);
-    if constexpr (!WARP) {
-        if ((threadIdx.x & 31) == 0)
-            red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = 0.0f;
-        for (int i = 0; i < nwarps; i += 4) {
-            const float4 t = *reinterpret_cast<const float4 *>(red + i);
-            v += (t.x + t.y) + (t.z + t.w);
-        }
+// A quad of parameters (all `def` where p is null); 0 from n on.
+template <int V>
+__device__ __forceinline__ void quad_params(const float *p, float def, int c, int S, int n, f2_t (&q)[2]) {
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = V == 4 ? c + i : c + i * S;
+        f[i] = at < n ? (p ? p[at] : def) : 0.0f;
     }
+    q[0] = f2_pack(f[0], f[1]);
+    q[1] = f2_pack(f[2], f[3]);
+}
+
+constexpr int kNormWideThreads = 512;
+
+// The sum of v over a block of kNormWideThreads, through `red` (one slot a warp).
+// Every thread adds the slots in the same order.
+__device__ __forceinline__ float wide_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNormWideThreads / 32; ++i)
+        v += red[i];
     return v;
 }
 
-// Zeroes `n` slots; the first barrier of row_sum's caller comes after it.
-__device__ __forceinline__ void clear_slots(float *red, int n) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        red[i] = 0.0f;
-    __syncthreads();
-}
-
-template <typename X, typename Y, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(norm_max_threads(NV *V, WARP, false), norm_min_blocks(NV *V, WARP, false))
+template <typename X, typename Y, int V, int NQ>
+__global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * NQ, false) / kNormBlockWarps)
     s6_layernorm_fwd_kernel(const NormFwdArgs a) {
-    using VX = IoVec<X, V>;
-    using VY = IoVec<Y, V>;
-    __shared__ __align__(16) float red[2][kNormMaxWarps];
-    if constexpr (!WARP)
-        clear_slots(red[0], 2 * kNormMaxWarps);
-    const int nwarps = blockDim.x >> 5;
-    const int G = WARP ? 32 : blockDim.x;                     // threads of a row
-    const int li = WARP ? (threadIdx.x & 31) : threadIdx.x;  // this thread among them
-    const int W = a.width;
+    using QX = Quad<X, V>;
+    using QY = Quad<Y, V>;
+    const int lane = threadIdx.x & 31, W = a.width;
+    auto col = [&](int j) { return lane * V + 128 * j; };  // of quad j
+    f2_t wv[NQ][2], bv[NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        quad_params<V>(a.w, 1.0f, col(j), 32, W, wv[j]);
+        quad_params<V>(a.b, 0.0f, col(j), 32, W, bv[j]);
+    }
+
+    const long long step = static_cast<long long>(kNormBlockWarps) * gridDim.x;
+    long long row = static_cast<long long>(kNormBlockWarps) * blockIdx.x + (threadIdx.x >> 5);
     const X *x = static_cast<const X *>(a.x);
     const Y *r = static_cast<const Y *>(a.r);
     X *s = static_cast<X *>(a.s);
     Y *y = static_cast<Y *>(a.y);
-
-    float wv[NV][V], bv[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (j * G + li) * V + i;
-            wv[j][i] = a.w && c < W ? a.w[c] : 1.0f;
-            bv[j][i] = a.b && c < W ? a.b[c] : 0.0f;
-        }
-
-    const long long per = WARP ? nwarps : 1;
-    const long long step = per * gridDim.x;
-    long long row = per * blockIdx.x + (WARP ? (threadIdx.x >> 5) : 0);
-    typename VX::raw xr[NV];
-    typename VY::raw rr[NV];
-    const int c0 = li * V, dc = G * V;  // this thread's first column, and from one to the next
+    QX xr[NQ];
+    QY rr[NQ];
     auto fetch = [&](long long at) {
-        const X *xp = x + at * W + c0;
-        const Y *rp = r + at * W + c0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = c0 + j * dc < W;
-            xr[j] = in ? VX::load(xp + j * dc) : VX::zero();
+        for (int j = 0; j < NQ; ++j) {
+            xr[j].template load<false>(x + at * W, col(j), 32, W);
             if (r)
-                rr[j] = in ? VY::load(rp + j * dc) : VY::zero();
+                rr[j].template load<false>(r + at * W, col(j), 32, W);
         }
     };
     if (row < a.rows)
         fetch(row);
     for (; row < a.rows; row += step) {
-        float v[NV][V], sum = 0.0f;
-        X *sp = s + row * W + c0;
-        Y *yp = y + row * W + c0;
+        f2_t v[NQ][2], t0 = f2_both(0.0f), t1 = t0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            VX::unpack(xr[j], v[j]);
+        for (int j = 0; j < NQ; ++j) {
+            xr[j].pairs(v[j]);
             if (r) {
-                float t[V];
-                VY::unpack(rr[j], t);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    v[j][i] += t[i];
-                if (s && c0 + j * dc < W)
-                    VX::store(sp + j * dc, VX::pack(v[j]));
+                f2_t t[2];
+                rr[j].pairs(t);
+                v[j][0] = f2_add(v[j][0], t[0]);
+                v[j][1] = f2_add(v[j][1], t[1]);
+                if (s)
+                    QX::template store<false>(s + row * W, col(j), 32, W, v[j]);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                sum += v[j][i];
+            t0 = f2_add(t0, v[j][0]);
+            t1 = f2_add(t1, v[j][1]);
         }
         if (row + step < a.rows)
             fetch(row + step);
-        const float mean = row_sum<WARP>(sum, red[0], nwarps) * a.inv_w;
+        const float mean = warp_sum(f2_sum(t0, t1)) * a.inv_w;
         // squares of the deviations from the mean, not of the values: a mean that is
         // large next to the deviations costs no digits
-        float sq = 0.0f;
+        t0 = t1 = f2_both(0.0f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (c0 + j * dc < W) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    v[j][i] -= mean;
-                    sq = fmaf(v[j][i], v[j][i], sq);
-                }
-            }
-        const float rstd = __frsqrt_rn(row_sum<WARP>(sq, red[1], nwarps) * a.inv_w + a.eps);
-        if (li == 0) {
+        for (int j = 0; j < NQ; ++j) {
+            f2_t m[2];
+            quad_where<V>(mean, col(j), 32, W, m);
+            v[j][0] = f2_sub(v[j][0], m[0]);
+            v[j][1] = f2_sub(v[j][1], m[1]);
+            t0 = f2_fma(v[j][0], v[j][0], t0);
+            t1 = f2_fma(v[j][1], v[j][1], t1);
+        }
+        const float rstd = __frsqrt_rn(warp_sum(f2_sum(t0, t1)) * a.inv_w + a.eps);
+        if (lane == 0) {
             if (a.mean)
                 a.mean[row] = mean;
             if (a.rstd)
                 a.rstd[row] = rstd;
         }
+        const f2_t q = f2_both(rstd);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (c0 + j * dc < W) {
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o[i] = fmaf(v[j][i] * rstd, wv[j][i], bv[j][i]);
-                VY::store(yp + j * dc, VY::pack(o));
-            }
+        for (int j = 0; j < NQ; ++j) {
+            const f2_t o[2] = {f2_fma(f2_mul(v[j][0], q), wv[j][0], bv[j][0]),
+                               f2_fma(f2_mul(v[j][1], q), wv[j][1], bv[j][1])};
+            QY::template store<false>(y + row * W, col(j), 32, W, o);
         }
     }
 }
 
-// Rows that do not fit a block's registers: a block walks its row three times
+// Rows above kNormMaxWidth: a block walks its row three times
 // (sum, squared deviations, output); the second and third reads hit L2.  s is
 // written on the last walk, since it may be x itself.
-constexpr int kNormWideThreads = 512;
-
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel(const NormFwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ __align__(16) float red[2][kNormMaxWarps];
+    __shared__ float red[2][kNormWideThreads / 32];
     const int W = a.width;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X *x = static_cast<const X *>(a.x) + row * W;
@@ -228,7 +210,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
             for (int i = 0; i < V; ++i)
                 sum += v[i];
         }
-        const float mean = row_sum<false>(sum, red[0], kNormWideThreads / 32) * a.inv_w;
+        const float mean = wide_sum(sum, red[0]) * a.inv_w;
         for (int c = threadIdx.x * V; c < W; c += kNormWideThreads * V) {
             float v[V];
             value(c, v);
@@ -236,7 +218,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
             for (int i = 0; i < V; ++i)
                 sq = fmaf(v[i] - mean, v[i] - mean, sq);
         }
-        const float rstd = __frsqrt_rn(row_sum<false>(sq, red[1], kNormWideThreads / 32) * a.inv_w + a.eps);
+        const float rstd = __frsqrt_rn(wide_sum(sq, red[1]) * a.inv_w + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean)
                 a.mean[row] = mean;
@@ -257,161 +239,442 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
 }
 
 // ----------------------------------------------------------------- backward
-// A thread owns the same columns of every row it meets, so dw and db stay in
-// its registers until the block's last row; the block then writes one row of
-// partial sums and s6_sum_parts_kernel adds those up.
-template <typename X, typename Y, int V, int NV, bool WARP>
-__global__ void __launch_bounds__(norm_max_threads(NV *V, WARP, true), norm_min_blocks(NV *V, WARP, true))
+// A lane owns the same columns of every row it meets, so dw and db stay in its
+// registers until the last one; the block then writes one row of partial sums
+// and s6_sum_parts_kernel adds those up.
+template <typename X, typename Y, int V, int NQ>
+__global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * NQ, true) / kNormBlockWarps)
     s6_layernorm_bwd_kernel(const NormBwdArgs a) {
-    using VX = IoVec<X, V>;
-    using VY = IoVec<Y, V>;
-    using VF = IoVec<float, V>;
-    __shared__ __align__(16) float red[2][2][kNormMaxWarps];
-    if constexpr (!WARP)
-        clear_slots(red[0][0], 4 * kNormMaxWarps);
-    const int nwarps = blockDim.x >> 5;
-    const int G = WARP ? 32 : blockDim.x;
-    const int li = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int W = a.width;
+    using QX = Quad<X, V>;
+    using QY = Quad<Y, V>;
+    using QF = Quad<float, V>;
+    const int lane = threadIdx.x & 31, W = a.width;
+    auto col = [&](int j) { return lane * V + 128 * j; };
+    f2_t wv[NQ][2], dw[NQ][2], db[NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        quad_params<V>(a.w, 1.0f, col(j), 32, W, wv[j]);
+        dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = f2_both(0.0f);
+    }
+
+    const long long step = static_cast<long long>(kNormBlockWarps) * gridDim.x;
+    long long row = static_cast<long long>(kNormBlockWarps) * blockIdx.x + (threadIdx.x >> 5);
     const X *x = static_cast<const X *>(a.x);
     const Y *dy = static_cast<const Y *>(a.dy);
-
-    float wv[NV][V], dw[NV][V], db[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (j * G + li) * V + i;
-            wv[j][i] = a.w && c < W ? a.w[c] : 1.0f;
-            dw[j][i] = 0.0f;
-            db[j][i] = 0.0f;
-        }
-
-    const long long per = WARP ? nwarps : 1;
-    const long long step = per * gridDim.x;
-    long long row = per * blockIdx.x + (WARP ? (threadIdx.x >> 5) : 0);
-    typename VX::raw xr[NV];
-    typename VY::raw gr[NV];
+    QX xr[NQ];
+    QY gr[NQ];
     float mean = 0.0f, rstd = 0.0f;
-    const int c0 = li * V, dc = G * V;
     auto fetch = [&](long long at) {
         mean = a.mean[at];
         rstd = a.rstd[at];
-        const X *xp = x + at * W + c0;
-        const Y *gp = dy + at * W + c0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = c0 + j * dc < W;
-            xr[j] = in ? VX::load(xp + j * dc) : VX::zero();
-            gr[j] = in ? VY::load(gp + j * dc) : VY::zero();
+        for (int j = 0; j < NQ; ++j) {
+            xr[j].template load<false>(x + at * W, col(j), 32, W);
+            gr[j].template load<false>(dy + at * W, col(j), 32, W);
         }
     };
     if (row < a.rows)
         fetch(row);
-    int turn = 0;
     for (; row < a.rows; row += step) {
-        float h[NV][V], g[NV][V], s0 = 0.0f, s1 = 0.0f;
-        const float q = rstd;
+        f2_t h[NQ][2], g[NQ][2], s0 = f2_both(0.0f), s1 = s0;
+        const f2_t m = f2_both(mean), q = f2_both(rstd);
+        const float rq = rstd;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            VX::unpack(xr[j], h[j]);
-            VY::unpack(gr[j], g[j]);
-            if (c0 + j * dc < W) {
+        for (int j = 0; j < NQ; ++j) {
+            xr[j].pairs(h[j]);
+            gr[j].pairs(g[j]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    h[j][i] = (h[j][i] - mean) * q;
-                    dw[j][i] = fmaf(g[j][i], h[j][i], dw[j][i]);
-                    db[j][i] += g[j][i];
-                    g[j][i] *= wv[j][i];
-                    s0 += g[j][i];
-                    s1 = fmaf(g[j][i], h[j][i], s1);
-                }
+            for (int i = 0; i < 2; ++i) {
+                // elements behind the row have g = 0 and add nothing
+                h[j][i] = f2_mul(f2_sub(h[j][i], m), q);
+                dw[j][i] = f2_fma(g[j][i], h[j][i], dw[j][i]);
+                db[j][i] = f2_add(db[j][i], g[j][i]);
+                g[j][i] = f2_mul(g[j][i], wv[j][i]);
+                s0 = f2_add(s0, g[j][i]);
+                s1 = f2_fma(g[j][i], h[j][i], s1);
             }
         }
         if (row + step < a.rows)
             fetch(row + step);
-        const float *dsp = a.ds + row * W + c0;
-        float *dxp = a.dx + row * W + c0;
-        typename VF::raw dsr[NV];
+        QF ds[NQ];
         if (a.ds) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                dsr[j] = c0 + j * dc < W ? VF::load(dsp + j * dc) : VF::zero();
+            for (int j = 0; j < NQ; ++j)
+                ds[j].template load<false>(a.ds + row * W, col(j), 32, W);
         }
-        s0 = warp_sum(s0);
-        s1 = warp_sum(s1);
-        if constexpr (!WARP) {
-            // two slots by turns: a slot is written again only after the barrier of the
-            // row between, which every reader of it has passed
-            float(*slot)[kNormMaxWarps] = red[turn];
-            turn ^= 1;
-            if ((threadIdx.x & 31) == 0) {
-                slot[0][threadIdx.x >> 5] = s0;
-                slot[1][threadIdx.x >> 5] = s1;
-            }
-            __syncthreads();
-            s0 = s1 = 0.0f;
-            for (int i = 0; i < nwarps; i += 4) {
-                const float4 t0 = *reinterpret_cast<const float4 *>(slot[0] + i);
-                const float4 t1 = *reinterpret_cast<const float4 *>(slot[1] + i);
-                s0 += (t0.x + t0.y) + (t0.z + t0.w);
-                s1 += (t1.x + t1.y) + (t1.z + t1.w);
-            }
-        }
-        const float m0 = s0 * a.inv_w, m1 = s1 * a.inv_w;
+        float m0, m1, hi;
+        f2_unpack(s0, m0, hi);
+        m0 += hi;
+        f2_unpack(s1, m1, hi);
+        m1 += hi;
+        warp_sum2(m0, m1);
+        // q (g - m0 - h m1) as q (g - h m1) - q m0
+        const f2_t c1 = f2_both(-m1 * a.inv_w), c0 = f2_both(-rq * (m0 * a.inv_w));
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (c0 + j * dc < W) {
-                float o[V];
+        for (int j = 0; j < NQ; ++j) {
+            f2_t o[2];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o[i] = q * (g[j][i] - fmaf(h[j][i], m1, m0));
-                if (a.ds) {
-                    float t[V];
-                    VF::unpack(dsr[j], t);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        o[i] += t[i];
-                }
-                VF::store(dxp + j * dc, VF::pack(o));
+            for (int i = 0; i < 2; ++i)
+                o[i] = f2_fma(f2_fma(h[j][i], c1, g[j][i]), q, c0);
+            if (a.ds) {
+                f2_t t[2];
+                ds[j].pairs(t);
+                o[0] = f2_add(o[0], t[0]);
+                o[1] = f2_add(o[1], t[1]);
             }
+            QF::template store<false>(a.dx + row * W, col(j), 32, W, o);
         }
     }
 
     if (!a.part)
         return;
-    float *part = a.part + static_cast<long long>(blockIdx.x) * 2 * W;
-    if constexpr (WARP) {
-        // the block's warps hold sums of the same columns: add them up in order
-        __shared__ float sums[2][kNormWarpWidth];
-        for (int k = 0; k < nwarps; ++k) {
-            if ((threadIdx.x >> 5) == k) {
+    // the block's warps hold sums of the same columns: add them up in order
+    __shared__ __align__(16) float sums[2][kNormWarpWidth];
+    for (int k = 0; k < kNormBlockWarps; ++k) {
+        if ((threadIdx.x >> 5) == k) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int c = (j * 32 + li) * V + i;
-                        sums[0][c] = k ? sums[0][c] + dw[j][i] : dw[j][i];
-                        sums[1][c] = k ? sums[1][c] + db[j][i] : db[j][i];
-                    }
-            }
-            __syncthreads();
-        }
-        for (int c = threadIdx.x; c < W; c += blockDim.x) {
-            part[c] = sums[0][c];
-            part[W + c] = sums[1][c];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (j * G + li) * V + i;
-                if (c < W) {
-                    part[c] = dw[j][i];
-                    part[W + c] = db[j][i];
+            for (int j = 0; j < NQ; ++j) {
+                f2_t t[2];
+                Quad<float, V> at;
+                if (k) {
+                    at.template load<true>(sums[0], col(j), 32, 0);
+                    at.pairs(t);
+                    dw[j][0] = f2_add(t[0], dw[j][0]);
+                    dw[j][1] = f2_add(t[1], dw[j][1]);
+                    at.template load<true>(sums[1], col(j), 32, 0);
+                    at.pairs(t);
+                    db[j][0] = f2_add(t[0], db[j][0]);
+                    db[j][1] = f2_add(t[1], db[j][1]);
                 }
+                QF::template store<true>(sums[0], col(j), 32, 0, dw[j]);
+                QF::template store<true>(sums[1], col(j), 32, 0, db[j]);
             }
+        }
+        __syncthreads();
+    }
+    float *part = a.part + static_cast<long long>(blockIdx.x) * 2 * W;
+    for (int c = threadIdx.x; c < W; c += 32 * kNormBlockWarps) {
+        part[c] = sums[0][c];
+        part[W + c] = sums[1][c];
+    }
+}
+
+// ------------------------------------------------ rows in shared memory
+// A copied row's buffer, as this thread's quads see it.  A row of an odd width
+// does not begin on a 16-byte boundary; the pieces around it that also hold the
+// neighbouring rows' bytes are read, never used.
+template <typename T>
+__device__ __forceinline__ const T *row_in(const unsigned char *buf, const T *tensor, long long at) {
+    return reinterpret_cast<const T *>(buf + in16(tensor, at));
+}
+
+// Forward: kNormStages rows of each warp in flight or in use; the copies of a
+// row are the lanes' own, so a warp waits for nothing but them.  w and b are
+// kept beside the rows.  Three passes over the row's buffer (sum, squared
+// deviations, output).
+constexpr int kNormStages = 2;
+constexpr int kNormRowWarps = 8;  // warps of a block, or as many as shared memory allows
+
+struct NormRowsArgs {
+    NormFwdArgs n;
+    int x_bytes, r_bytes;  // row buffers
+};
+
+template <typename X, typename Y, int V>
+__global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kernel(const NormRowsArgs args) {
+    using QX = Quad<X, V>;
+    using QY = Quad<Y, V>;
+    using QF = Quad<float, V>;
+    const NormFwdArgs &a = args.n;
+    extern __shared__ __align__(16) unsigned char s6_norm_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int W = a.width, c0 = lane * V;
+    const int whole = W & ~127;  // columns of whole steps of the warp: a quad a lane
+    float *w = reinterpret_cast<float *>(s6_norm_smem), *b = w + (W + 3) / 4 * 4;
+    const int stage = args.x_bytes + args.r_bytes;
+    unsigned char *rows = reinterpret_cast<unsigned char *>(b + (W + 3) / 4 * 4) + warp * kNormStages * stage;
+    const X *x = static_cast<const X *>(a.x);
+    const Y *r = static_cast<const Y *>(a.r);
+
+    const long long step = static_cast<long long>(warps) * gridDim.x;
+    long long row = static_cast<long long>(warps) * blockIdx.x + warp;
+    auto fetch = [&](int st, long long at) {
+        if (at < a.rows) {
+            row_copy(rows + st * stage, x + at * W, W, x, lane, 32);
+            if (r)
+                row_copy(rows + st * stage + args.x_bytes, r + at * W, W, r, lane, 32);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kNormStages; ++st)
+        fetch(st, row + st * step);
+    for (int c = threadIdx.x; c < W; c += blockDim.x) {
+        w[c] = a.w ? a.w[c] : 1.0f;
+        b[c] = a.b ? a.b[c] : 0.0f;
+    }
+    __syncthreads();
+
+    for (int st = 0; row < a.rows; row += step, st = st + 1 == kNormStages ? 0 : st + 1) {
+        cp_async_wait<kNormStages - 1>();
+        __syncwarp();
+        const X *xs = row_in(rows + st * stage, x, row * W);
+        const Y *rs = r ? row_in(rows + st * stage + args.x_bytes, r, row * W) : nullptr;
+        auto value = [&](auto all, int c, f2_t (&v)[2]) {
+            constexpr bool ALL = decltype(all)::value;
+            QX q;
+            q.template load<ALL>(xs, c, 32, W);
+            q.pairs(v);
+            if (r) {
+                QY p;
+                f2_t t[2];
+                p.template load<ALL>(rs, c, 32, W);
+                p.pairs(t);
+                v[0] = f2_add(v[0], t[0]);
+                v[1] = f2_add(v[1], t[1]);
+            }
+        };
+        // fn(all, column) for the whole steps, then for the one that the row's end cuts
+        auto walk = [&](auto fn) {
+#pragma unroll 4
+            for (int c = 0; c < whole; c += 128)
+                fn(std::true_type{}, c0 + c);
+            if (whole < W)
+                fn(std::false_type{}, c0 + whole);
+        };
+        f2_t t0 = f2_both(0.0f), t1 = t0;
+        walk([&](auto all, int c) {
+            f2_t v[2];
+            value(all, c, v);
+            t0 = f2_add(t0, v[0]);
+            t1 = f2_add(t1, v[1]);
+        });
+        const float mean = warp_sum(f2_sum(t0, t1)) * a.inv_w;
+        t0 = t1 = f2_both(0.0f);
+        walk([&](auto all, int c) {
+            f2_t v[2], m[2] = {f2_both(mean), f2_both(mean)};
+            value(all, c, v);
+            if constexpr (!decltype(all)::value)
+                quad_where<V>(mean, c, 32, W, m);
+            v[0] = f2_sub(v[0], m[0]);
+            v[1] = f2_sub(v[1], m[1]);
+            t0 = f2_fma(v[0], v[0], t0);
+            t1 = f2_fma(v[1], v[1], t1);
+        });
+        const float rstd = __frsqrt_rn(warp_sum(f2_sum(t0, t1)) * a.inv_w + a.eps);
+        if (lane == 0) {
+            if (a.mean)
+                a.mean[row] = mean;
+            if (a.rstd)
+                a.rstd[row] = rstd;
+        }
+        X *sp = a.s ? static_cast<X *>(a.s) + row * W : nullptr;
+        Y *yp = static_cast<Y *>(a.y) + row * W;
+        const f2_t m = f2_both(mean), q = f2_both(rstd);
+        walk([&](auto all, int c) {
+            constexpr bool ALL = decltype(all)::value;
+            f2_t v[2], wv[2], bv[2];
+            value(all, c, v);
+            if (sp)
+                QX::template store<ALL>(sp, c, 32, W, v);
+            QF p;
+            p.template load<ALL>(w, c, 32, W);
+            p.pairs(wv);
+            p.template load<ALL>(b, c, 32, W);
+            p.pairs(bv);
+            const f2_t o[2] = {f2_fma(f2_mul(f2_sub(v[0], m), q), wv[0], bv[0]),
+                               f2_fma(f2_mul(f2_sub(v[1], m), q), wv[1], bv[1])};
+            QY::template store<ALL>(yp, c, 32, W, o);
+        });
+        __syncwarp();  // every lane is done with the stage
+        fetch(st, row + kNormStages * step);
+    }
+}
+
+// Backward: a block takes `tile` rows at a time, kNormStages tiles in flight or
+// in use.  Each row's two sums are made by blockDim / 32 / tile warps, whose
+// parts every thread then adds in order; a thread owns NQ quads of columns and
+// keeps their dw and db in registers until the block's last tile.  Blocks have a
+// multiple of 4 warps, one for each scheduler of the SM: with 5 (which a width
+// of 2560 would fill exactly) the busiest one had 1.3 times its share.
+struct NormTileArgs {
+    NormBwdArgs n;
+    int tile;
+    int x_bytes, dy_bytes, ds_bytes;  // row buffers
+};
+
+constexpr int kNormTileRows = 8;  // at most
+
+template <typename X, typename Y, int V, int NQ, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const NormTileArgs args) {
+    using QX = Quad<X, V>;
+    using QY = Quad<Y, V>;
+    using QF = Quad<float, V>;
+    const NormBwdArgs &a = args.n;
+    extern __shared__ __align__(16) unsigned char s6_norm_smem[];
+    __shared__ float stats[kNormStages][kNormTileRows][2];  // mean, rstd
+    __shared__ float2 parts[kNormTileRows][MAXT / 32];      // each warp's two sums
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int W = a.width, T = blockDim.x, R = args.tile;
+    const int share = warps / R;  // warps that sum a row
+    float *w = reinterpret_cast<float *>(s6_norm_smem);
+    const int rb = args.x_bytes + args.dy_bytes + args.ds_bytes;
+    unsigned char *buf = reinterpret_cast<unsigned char *>(w + (W + 3) / 4 * 4);
+    const X *x = static_cast<const X *>(a.x);
+    const Y *dy = static_cast<const Y *>(a.dy);
+    auto col = [&](int j) { return static_cast<int>(threadIdx.x) * V + 4 * T * j; };
+
+    const long long tiles = (a.rows + R - 1) / R;
+    auto fetch = [&](int st, long long tile) {
+        if (tile < tiles) {
+            for (int k = 0; k < R; ++k) {
+                const long long row = tile * R + k;
+                if (row >= a.rows)
+                    break;
+                unsigned char *to = buf + (st * R + k) * rb;
+                row_copy(to, x + row * W, W, x, threadIdx.x, T);
+                row_copy(to + args.x_bytes, dy + row * W, W, dy, threadIdx.x, T);
+                if (a.ds)
+                    row_copy(to + args.x_bytes + args.dy_bytes, a.ds + row * W, W, a.ds, threadIdx.x, T);
+            }
+            const int k = threadIdx.x;
+            if (k < R && tile * R + k < a.rows) {
+                cp_async4(&stats[st][k][0], a.mean + tile * R + k);
+                cp_async4(&stats[st][k][1], a.rstd + tile * R + k);
+            }
+        }
+        cp_async_commit();
+    };
+    long long tile = blockIdx.x;
+#pragma unroll
+    for (int st = 0; st < kNormStages; ++st)
+        fetch(st, tile + static_cast<long long>(st) * gridDim.x);
+    for (int c = threadIdx.x; c < W; c += T)
+        w[c] = a.w ? a.w[c] : 1.0f;
+    f2_t wv[NQ][2], dw[NQ][2], db[NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        quad_params<V>(a.w, 1.0f, col(j), T, W, wv[j]);
+        dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = f2_both(0.0f);
+    }
+
+    for (int st = 0; tile < tiles; tile += gridDim.x, st = st + 1 == kNormStages ? 0 : st + 1) {
+        const int here = a.rows - tile * R < R ? static_cast<int>(a.rows - tile * R) : R;
+        cp_async_wait<kNormStages - 1>();
+        __syncthreads();
+        const unsigned char *rows = buf + st * R * rb;
+        if (warp / share < here) {
+            const int k = warp / share, part = warp - k * share;
+            const long long at = (tile * R + k) * W;
+            const X *xs = row_in(rows + k * rb, x, at);
+            const Y *gs = row_in(rows + k * rb + args.x_bytes, dy, at);
+            const f2_t m = f2_both(stats[st][k][0]), q = f2_both(stats[st][k][1]);
+            f2_t s0 = f2_both(0.0f), s1 = s0;
+            auto one = [&](auto all, int c) {
+                constexpr bool ALL = decltype(all)::value;
+                QX xq;
+                QY gq;
+                QF wq;
+                f2_t h[2], g[2], wc[2];
+                xq.template load<ALL>(xs, c, 32, W);
+                gq.template load<ALL>(gs, c, 32, W);
+                wq.template load<ALL>(w, c, 32, W);
+                xq.pairs(h);
+                gq.pairs(g);
+                wq.pairs(wc);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    g[i] = f2_mul(g[i], wc[i]);
+                    s0 = f2_add(s0, g[i]);
+                    s1 = f2_fma(g[i], f2_mul(f2_sub(h[i], m), q), s1);
+                }
+            };
+            int c = part * 128;
+#pragma unroll 4
+            for (; c + 128 <= W; c += share * 128)
+                one(std::true_type{}, c + lane * V);
+            if (c < W)
+                one(std::false_type{}, c + lane * V);
+            float m0, m1, hi;
+            f2_unpack(s0, m0, hi);
+            m0 += hi;
+            f2_unpack(s1, m1, hi);
+            m1 += hi;
+            warp_sum2(m0, m1);
+            if (lane == 0)
+                parts[k][part] = make_float2(m0, m1);
+        }
+        __syncthreads();
+        float *dxp = a.dx + tile * R * W;
+        for (int k = 0; k < here; ++k, dxp += W) {
+            const long long at = (tile * R + k) * W;
+            const X *xs = row_in(rows + k * rb, x, at);
+            const Y *gs = row_in(rows + k * rb + args.x_bytes, dy, at);
+            const float *es = row_in(rows + k * rb + args.x_bytes + args.dy_bytes, a.ds, at);
+            const float rstd = stats[st][k][1];
+            const f2_t m = f2_both(stats[st][k][0]), q = f2_both(rstd);
+            float m0 = 0.0f, m1 = 0.0f;
+            for (int p = 0; p < share; ++p) {
+                m0 += parts[k][p].x;
+                m1 += parts[k][p].y;
+            }
+            const f2_t c1 = f2_both(-m1 * a.inv_w), c0 = f2_both(-rstd * (m0 * a.inv_w));
+            auto one = [&](auto all, int j) {
+                constexpr bool ALL = decltype(all)::value;
+                QX xq;
+                QY gq;
+                f2_t h[2], g[2], o[2];
+                xq.template load<ALL>(xs, col(j), T, W);
+                gq.template load<ALL>(gs, col(j), T, W);
+                xq.pairs(h);
+                gq.pairs(g);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    h[i] = f2_mul(f2_sub(h[i], m), q);
+                    dw[j][i] = f2_fma(g[i], h[i], dw[j][i]);
+                    db[j][i] = f2_add(db[j][i], g[i]);
+                    o[i] = f2_fma(f2_fma(h[i], c1, f2_mul(g[i], wv[j][i])), q, c0);
+                }
+                if (a.ds) {
+                    QF eq;
+                    f2_t t[2];
+                    eq.template load<ALL>(es, col(j), T, W);
+                    eq.pairs(t);
+                    o[0] = f2_add(o[0], t[0]);
+                    o[1] = f2_add(o[1], t[1]);
+                }
+                QF::template store<ALL>(dxp, col(j), T, W, o);
+            };
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                if (4 * T * (j + 1) <= W)
+                    one(std::true_type{}, j);
+                else if (4 * T * j < W)
+                    one(std::false_type{}, j);
+            }
+        }
+        __syncthreads();  // every thread is done with the stage
+        fetch(st, tile + static_cast<long long>(kNormStages) * gridDim.x);
+    }
+    if (!a.part)
+        return;
+    float *part = a.part + static_cast<long long>(blockIdx.x) * 2 * W;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        // part's rows are W floats: single elements keep any alignment
+        float f[4], g[4];
+        f2_unpack(dw[j][0], f[0], f[1]);
+        f2_unpack(dw[j][1], f[2], f[3]);
+        f2_unpack(db[j][0], g[0], g[1]);
+        f2_unpack(db[j][1], g[2], g[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = V == 4 ? col(j) + i : col(j) + i * T;
+            if (c < W) {
+                part[c] = f[i];
+                part[W + c] = g[i];
+            }
+        }
     }
 }
 
@@ -421,7 +684,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_k
                                                                                     float2 *sums) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ __align__(16) float red[2][kNormMaxWarps];
+    __shared__ float red[2][kNormWideThreads / 32];
     const int W = a.width;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X *x = static_cast<const X *>(a.x) + row * W;
@@ -439,8 +702,8 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_k
                 s1 = fmaf(t, (h[i] - mean) * rstd, s1);
             }
         }
-        s0 = row_sum<false>(s0, red[0], kNormWideThreads / 32);
-        s1 = row_sum<false>(s1, red[1], kNormWideThreads / 32);
+        s0 = wide_sum(s0, red[0]);
+        s1 = wide_sum(s1, red[1]);
         if (threadIdx.x == 0)
             sums[row] = make_float2(s0 * a.inv_w, s1 * a.inv_w);
     }

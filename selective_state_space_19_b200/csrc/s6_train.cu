@@ -81,29 +81,66 @@ int check_norm_dims(const s6_norm_dims *dims) {
     return S6_OK;
 }
 
+// Blocks that fit an SM beside one another with `smem` bytes each (227 KB in all,
+// 1 KB of it the system's for each block).
+constexpr int kSmemSM = 227 * 1024, kSmemBlock = 1024;
+int64_t blocks_of_smem(int64_t smem) { return std::max<int64_t>(1, kSmemSM / (smem + kSmemBlock)); }
+
 struct NormPlan {
-    int warps;  // warps that share a row; 1: a row a warp, kNormBlockWarps rows a block
     int elems;  // elements of a row that a thread holds, at most
     int threads;
-    int64_t blocks;
+    int tile;   // rows that a block takes at a time (backward through shared memory)
+    int64_t blocks, smem;
 };
 
-// One warp a row up to kNormWarpWidth elements, above that as many warps as hold the
-// row; as many blocks as are resident, which walk the rows.
-NormPlan norm_plan(int64_t rows, int64_t width, bool bwd) {
+// Rows of one warp: as many blocks as are resident, which walk the rows.
+NormPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd) {
     NormPlan p;
-    if (width <= s6::kNormWarpWidth) {
-        p.warps = 1;
-        p.elems = static_cast<int>(4 * ceil_div(width, 128));
-        p.threads = 32 * s6::kNormBlockWarps;
-        p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps),
-                            kSMs * s6::norm_warps_resident(p.elems, true, bwd) / s6::kNormBlockWarps);
-    } else {
-        p.elems = s6::norm_block_elems(width, bwd);
-        p.warps = static_cast<int>(ceil_div(width, 32 * p.elems));
-        p.threads = 32 * p.warps;
-        p.blocks = std::min(rows, kSMs * (s6::norm_warps_resident(p.elems, false, bwd) / p.warps));
-    }
+    p.elems = static_cast<int>(4 * ceil_div(width, 128));
+    p.threads = 32 * s6::kNormBlockWarps;
+    p.tile = p.smem = 0;
+    p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps),
+                        kSMs * s6::norm_warps_resident(p.elems, bwd) / s6::kNormBlockWarps);
+    return p;
+}
+
+// Blocks of the backward through shared memory on an SM, at 128 registers a thread.
+constexpr int norm_tile_resident(int64_t warps) { return static_cast<int>(16 / warps); }
+
+int64_t norm_params_bytes(int64_t width) { return (width + 3) / 4 * 4 * static_cast<int64_t>(sizeof(float)); }
+
+// Forward through shared memory: 8 warps where two blocks of them fit an SM, or
+// else as many as one block can have.
+NormPlan norm_rows_plan(int64_t rows, int64_t width, int64_t row_bytes) {
+    NormPlan p;
+    p.elems = p.tile = 0;
+    const int64_t fixed = 2 * norm_params_bytes(width), warp = s6::kNormStages * row_bytes;
+    int64_t warps = s6::kNormRowWarps;
+    while (warps > 1 && fixed + warps * warp > kSmemSM - kSmemBlock)
+        warps /= 2;
+    p.threads = static_cast<int>(32 * warps);
+    p.smem = fixed + warps * warp;
+    p.blocks = std::min(ceil_div(rows, warps), kSMs * std::min<int64_t>(blocks_of_smem(p.smem), 2));
+    return p;
+}
+
+// Backward through shared memory: 4, 8 or 16 warps with as many quads of columns a
+// thread as hold the row; then the most rows of a tile that leave room for the
+// blocks that the registers allow on an SM.
+NormPlan norm_tile_plan(int64_t rows, int64_t width, int64_t row_bytes) {
+    NormPlan p;
+    const int64_t quads = ceil_div(width, 128);  // of a warp
+    const int64_t warps = quads <= 16 ? 4 : quads <= 32 ? 8 : 16;
+    p.elems = static_cast<int>(4 * ceil_div(quads, warps));
+    const int64_t fixed = norm_params_bytes(width), most = norm_tile_resident(warps);
+    const int64_t statics = 2 * kSmemBlock;  // the kernel's own shared arrays and the system's part
+    int64_t tile = std::min<int64_t>(s6::kNormTileRows, warps);
+    while (tile > 1 && fixed + s6::kNormStages * tile * row_bytes > kSmemSM / std::min<int64_t>(most, 3) - statics)
+        tile /= 2;
+    p.tile = static_cast<int>(tile);
+    p.threads = static_cast<int>(32 * warps);
+    p.smem = fixed + s6::kNormStages * tile * row_bytes;
+    p.blocks = std::min(ceil_div(rows, tile), kSMs * std::min(blocks_of_smem(p.smem + kSmemBlock), most));
     return p;
 }
 
@@ -114,34 +151,39 @@ int64_t norm_wide_runs(int64_t rows, int64_t width) {
     return std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
 }
 
-template <typename X, typename Y, int V, int NV, bool WARP>
-int norm_launch(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    s6::s6_layernorm_fwd_kernel<X, Y, V, NV, WARP><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
-    return launch_status(cudaGetLastError());
+template <typename X, typename Y, int V, int NQ>
+void norm_launch(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    s6::s6_layernorm_fwd_kernel<X, Y, V, NQ><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
 }
 
-template <typename X, typename Y, int V, int NV, bool WARP>
-int norm_launch(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    s6::s6_layernorm_bwd_kernel<X, Y, V, NV, WARP><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
-    return launch_status(cudaGetLastError());
+template <typename X, typename Y, int V, int NQ>
+void norm_launch(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
+    s6::s6_layernorm_bwd_kernel<X, Y, V, NQ><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
 }
 
-// The instantiation that holds p.elems elements a thread, as vectors of V.
+// Rows of one warp: the instantiation that holds p.elems elements a lane.
 template <typename X, typename Y, int V, typename Args>
-int norm_dispatch(const Args &a, const NormPlan &p, cudaStream_t st) {
-    if (p.warps == 1) {
-        if (p.elems <= 4)
-            return norm_launch<X, Y, V, 4 / V, true>(a, p, st);
-        if (p.elems <= 8)
-            return norm_launch<X, Y, V, 8 / V, true>(a, p, st);
-        if (p.elems <= 12)
-            return norm_launch<X, Y, V, 12 / V, true>(a, p, st);
-        return norm_launch<X, Y, V, 16 / V, true>(a, p, st);
-    }
-    if constexpr (std::is_same<Args, s6::NormBwdArgs>::value)
-        if (p.elems > 8)
-            return norm_launch<X, Y, V, 16 / V, false>(a, p, st);
-    return norm_launch<X, Y, V, 8 / V, false>(a, p, st);
+int norm_warp_rows(const Args &a, const NormPlan &p, cudaStream_t st) {
+    if (p.elems <= 4)
+        norm_launch<X, Y, V, 1>(a, p, st);
+    else if (p.elems <= 8)
+        norm_launch<X, Y, V, 2>(a, p, st);
+    else if (p.elems <= 12)
+        norm_launch<X, Y, V, 3>(a, p, st);
+    else
+        norm_launch<X, Y, V, 4>(a, p, st);
+    return launch_status(cudaGetLastError());
+}
+
+// Launches a kernel with more dynamic shared memory than the default 48 KB (the
+// attribute is the device's own, and setting it costs little).
+template <typename Args>
+int launch_smem(void (*kern)(Args), const NormPlan &p, cudaStream_t st, const Args &a) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem)) !=
+        cudaSuccess)
+        return S6_ERR_CUDA;
+    kern<<<static_cast<unsigned>(p.blocks), p.threads, static_cast<size_t>(p.smem), st>>>(a);
+    return launch_status(cudaGetLastError());
 }
 
 template <typename X, typename Y, int V>
@@ -152,7 +194,31 @@ int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
             <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a);
         return launch_status(cudaGetLastError());
     }
-    return norm_dispatch<X, Y, V>(a, norm_plan(a.rows, a.width, false), st);
+    if (a.width <= s6::kNormWarpWidth)
+        return norm_warp_rows<X, Y, V>(a, norm_warp_plan(a.rows, a.width, false), st);
+    s6::NormRowsArgs r;
+    r.n = a;
+    r.x_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(X)));
+    r.r_bytes = a.r ? s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(Y))) : 0;
+    return launch_smem(s6::s6_layernorm_fwd_rows_kernel<X, Y, V>,
+                       norm_rows_plan(a.rows, a.width, r.x_bytes + r.r_bytes), st, r);
+}
+
+// Quads of a thread and threads of a block: 2 to 4 with 4 warps (widths up to 2048),
+// 3 or 4 with 8 and with 16.
+template <typename X, typename Y, int V, int NQ, int T>
+int norm_tile_t(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
+    return launch_smem(s6::s6_layernorm_bwd_tile_kernel<X, Y, V, NQ, T, norm_tile_resident(T / 32)>, p, st, a);
+}
+template <typename X, typename Y, int V>
+int norm_tile(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
+    if (p.threads == 128)
+        return p.elems <= 8    ? norm_tile_t<X, Y, V, 2, 128>(a, p, st)
+               : p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 128>(a, p, st)
+                               : norm_tile_t<X, Y, V, 4, 128>(a, p, st);
+    if (p.threads == 256)
+        return p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 256>(a, p, st) : norm_tile_t<X, Y, V, 4, 256>(a, p, st);
+    return p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 512>(a, p, st) : norm_tile_t<X, Y, V, 4, 512>(a, p, st);
 }
 
 template <typename X, typename Y, int V>
@@ -173,10 +239,23 @@ int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db,
                         static_cast<unsigned>(parts));
         s6::s6_layernorm_bwd_wide_cols_kernel<X, Y, V><<<grid, s6::kNormColThreads, 0, st>>>(a, sums);
     } else {
-        const NormPlan p = norm_plan(a.rows, a.width, true);
-        parts = p.blocks;
         a.part = params ? part : nullptr;
-        const int rc = norm_dispatch<X, Y, V>(a, p, st);
+        int rc;
+        if (a.width <= s6::kNormWarpWidth) {
+            const NormPlan p = norm_warp_plan(a.rows, a.width, true);
+            parts = p.blocks;
+            rc = norm_warp_rows<X, Y, V>(a, p, st);
+        } else {
+            s6::NormTileArgs t;
+            t.n = a;
+            t.x_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(X)));
+            t.dy_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(Y)));
+            t.ds_bytes = a.ds ? s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(float))) : 0;
+            const NormPlan p = norm_tile_plan(a.rows, a.width, t.x_bytes + t.dy_bytes + t.ds_bytes);
+            parts = p.blocks;
+            t.tile = p.tile;
+            rc = norm_tile<X, Y, V>(t, p, st);
+        }
         if (rc != S6_OK)
             return rc;
     }
@@ -460,7 +539,14 @@ int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims) {
     const int64_t row = 2 * dims->width * static_cast<int64_t>(sizeof(float));
     if (dims->width > s6::kNormMaxWidth)
         return dims->rows * static_cast<int64_t>(sizeof(float2)) + norm_wide_runs(dims->rows, dims->width) * row;
-    return norm_plan(dims->rows, dims->width, true).blocks * row;
+    if (dims->width <= s6::kNormWarpWidth)
+        return norm_warp_plan(dims->rows, dims->width, true).blocks * row;
+    // with or without ds: the smaller rows may give more blocks, or the larger ones (shorter tiles)
+    const int64_t io = s6::row_buffer_bytes(dims->width * static_cast<int64_t>(io_size(dims->x_dtype))) +
+                       s6::row_buffer_bytes(dims->width * static_cast<int64_t>(io_size(dims->y_dtype)));
+    const int64_t ds = s6::row_buffer_bytes(dims->width * static_cast<int64_t>(sizeof(float)));
+    return row * std::max(norm_tile_plan(dims->rows, dims->width, io).blocks,
+                          norm_tile_plan(dims->rows, dims->width, io + ds).blocks);
 }
 
 int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd, const float *w,

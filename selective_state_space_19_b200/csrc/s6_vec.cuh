@@ -64,11 +64,140 @@ struct IoVec {
     }
 };
 
+// ------------------------------------------------------- quads of a row
+// Four elements of a row in one thread, as two float32 pairs.  V = 4: a vector,
+// elements c .. c+3 (c and the row's length multiples of 4, rows aligned to
+// vectors).  V = 1: the elements c, c + S, c + 2S, c + 3S.  Elements from n on
+// are not touched and read as zero; ALL says that there are none.
+template <typename T, int V>
+struct Quad {
+    using Vec = IoVec<T, V>;
+    typename Vec::raw r[4 / V];
+
+    template <bool ALL>
+    __device__ __forceinline__ void load(const T *p, int c, int S, int n) {
+#pragma unroll
+        for (int i = 0; i < 4 / V; ++i)
+            r[i] = ALL || c + i * S < n ? Vec::load(p + c + i * S) : Vec::zero();
+    }
+    __device__ __forceinline__ void pairs(f2_t (&q)[2]) const {
+        if constexpr (sizeof(T) == 2 && V == 4) {
+            // bfloat16 to float32: its bits are the top half
+            q[0] = f2_pack(__uint_as_float(r[0].x << 16), __uint_as_float(r[0].x & 0xffff0000u));
+            q[1] = f2_pack(__uint_as_float(r[0].y << 16), __uint_as_float(r[0].y & 0xffff0000u));
+        } else if constexpr (V == 4) {
+            q[0] = f2_pack(__uint_as_float(r[0].x), __uint_as_float(r[0].y));
+            q[1] = f2_pack(__uint_as_float(r[0].z), __uint_as_float(r[0].w));
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                q[i] = f2_pack(__uint_as_float(static_cast<uint32_t>(r[2 * i]) << 16),
+                               __uint_as_float(static_cast<uint32_t>(r[2 * i + 1]) << 16));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                q[i] = f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        }
+    }
+    template <bool ALL>
+    static __device__ __forceinline__ void store(T *p, int c, int S, int n, const f2_t (&q)[2]) {
+        float f[4];
+        f2_unpack(q[0], f[0], f[1]);
+        f2_unpack(q[1], f[2], f[3]);
+        if constexpr (V == 4) {
+            if (ALL || c < n)
+                Vec::store(p + c, Vec::pack(f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (ALL || c + i * S < n)
+                    p[c + i * S] = io_traits<T>::from_f(f[i]);
+        }
+    }
+};
+
+// A value where the quad's elements are below n, 0 elsewhere.
+template <int V>
+__device__ __forceinline__ void quad_where(float v, int c, int S, int n, f2_t (&q)[2]) {
+    if constexpr (V == 4) {
+        q[0] = q[1] = c < n ? f2_pack(v, v) : f2_pack(0.0f, 0.0f);
+    } else {
+        q[0] = f2_pack(c < n ? v : 0.0f, c + S < n ? v : 0.0f);
+        q[1] = f2_pack(c + 2 * S < n ? v : 0.0f, c + 3 * S < n ? v : 0.0f);
+    }
+}
+
+__device__ __forceinline__ f2_t f2_both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float f2_sum(f2_t a, f2_t b) {
+    float x, y;
+    f2_unpack(f2_add(a, b), x, y);
+    return x + y;
+}
+
+// ------------------------------------------------- rows into shared memory
+// 16-byte asynchronous copy of the first `bytes` (1 .. 16) at src; the rest of
+// dst reads as zero.  Both addresses 16-byte aligned.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Shared bytes that a row of n bytes may take: it keeps its place within 16 bytes.
+__host__ __device__ constexpr int row_buffer_bytes(long long n) { return static_cast<int>((n + 15) / 16 * 16 + 16); }
+
+// The place of an address within 16 bytes; that of element `at` of a tensor.
+__device__ __forceinline__ int in16(const void *p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u); }
+template <typename T>
+__device__ __forceinline__ int in16(const T *p, long long at) {
+    return static_cast<int>((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) +
+                             static_cast<uint32_t>(at) * static_cast<uint32_t>(sizeof(T))) & 15u);
+}
+
+// Starts copying the n elements at src into buf, src's place within 16 bytes
+// kept (element 0 lands at buf + in16(src)), by `threads` threads of index t.
+// The copies begin on a 16-byte boundary, so up to 15 bytes in front of the row
+// come along: the end of the row before it, or, where the tensor itself (at
+// `tensor`) begins off the boundary, nothing: that one copy is made of elements.
+template <typename T>
+__device__ __forceinline__ void row_copy(unsigned char *buf, const T *src, int n, const void *tensor, int t,
+                                         int threads) {
+    const int at = in16(src), total = at + n * static_cast<int>(sizeof(T));
+    const unsigned char *from = reinterpret_cast<const unsigned char *>(src) - at;
+    for (int k = t * 16; k < total; k += threads * 16) {
+        if (k > 0 || from >= static_cast<const unsigned char *>(tensor)) {
+            cp_async16(buf + k, from + k, total - k < 16 ? total - k : 16);
+        } else {
+            for (int i = at; i < 16 && i < total; i += sizeof(T))
+                *reinterpret_cast<T *>(buf + i) = *reinterpret_cast<const T *>(from + i);
+        }
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+// Two sums over a warp in one walk: lanes 0-15 go on with the first, 16-31 with
+// the second, and every lane receives both.
+__device__ __forceinline__ void warp_sum2(float &a, float &b) {
+    const bool low = (threadIdx.x & 16) == 0;
+    float v = low ? a : b;
+    v += __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
 }
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll

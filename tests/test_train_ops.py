@@ -49,7 +49,7 @@ TYPES = [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")]
 # odd widths on each side of it, and the widest rows with their wide form
 SHAPES = [(1, 1), (3, 2), (5, 8), (1, 384), (300, 384), (9, 130), (37, 500), (2, 512), (4, 513), (3, 516),
           (21, 1001), (33, 1536), (2500, 64), (5, 2560), (3, 2561), (2, 8192), (2, 8191), (2, 8196), (3, 8193),
-          (1, 20000)]
+          (1, 20000), (7001, 516), (2500, 1031), (1300, 2568)]
 
 
 @pytest.mark.parametrize("add", [False, True])
