@@ -21,6 +21,9 @@
 #include "s6_bwd_rev.cuh"
 #include "s6_block.cuh"
 
+// The device error word of the training-step operators (s6_train.cu).
+cudaError_t s6_train_error_word(void **word);
+
 namespace {
 
 using namespace s6::host;
@@ -1345,19 +1348,23 @@ int s6_block_step(const s6_block_dims *dims, const s6_block_weights *w, float *x
 // (synchronises `stream`).  S6_ERR_TIMEOUT if a bounded wait gave up.
 int s6_device_status(s6_stream_t stream) {
     DeviceRestore restore_device;
-    unsigned int v = 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (use_stream_device(s) != S6_OK)
         return S6_ERR_CUDA;
-    if (cudaMemcpyFromSymbolAsync(&v, s6::g_s6_device_error, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess)
+    void *word[2];
+    unsigned int v[2] = {0, 0};
+    if (cudaGetSymbolAddress(&word[0], s6::g_s6_device_error) != cudaSuccess ||
+        s6_train_error_word(&word[1]) != cudaSuccess)
         return S6_ERR_CUDA;
+    for (int i = 0; i < 2; ++i)
+        if (cudaMemcpyAsync(&v[i], word[i], sizeof(v[i]), cudaMemcpyDeviceToHost, s) != cudaSuccess)
+            return S6_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess)
         return S6_ERR_CUDA;
-    if (v) {
-        const unsigned int zero = 0;
-        if (cudaMemcpyToSymbolAsync(s6::g_s6_device_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) !=
-            cudaSuccess)
-            return S6_ERR_CUDA;
+    if (v[0] || v[1]) {
+        for (int i = 0; i < 2; ++i)
+            if (cudaMemsetAsync(word[i], 0, sizeof(v[i]), s) != cudaSuccess)
+                return S6_ERR_CUDA;
         cudaStreamSynchronize(s);
         return S6_ERR_TIMEOUT;
     }

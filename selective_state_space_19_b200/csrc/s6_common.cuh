@@ -330,10 +330,9 @@ __device__ __forceinline__ void st_release_gpu(unsigned int *p, unsigned int v) 
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// Device-side error word of s6_abi.cu, whose kernels hold all of the library's
-// bounded waits (static: a translation unit without such waits has a word that
-// nothing sets).  Bit 0: a bounded wait gave up.  Read and cleared by the host
-// through s6_device_status.
+// Device-side error word, one for each translation unit (s6_abi.cu, s6_train.cu)
+// and device.  Bit 0: a bounded wait gave up.  Both are read and cleared by the
+// host through s6_device_status.
 static __device__ unsigned int g_s6_device_error = 0;
 
 __device__ __forceinline__ void raise_device_error(unsigned int bits) { atomicOr(&g_s6_device_error, bits); }

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     const int d = a.d, L = a.L;
 
     f2_t w[K][P], cb[P], dw[K][P], db[P];
-    const f2_t zero = f2_pack(0.0f, 0.0f), one = f2_pack(1.0f, 1.0f);
+    const f2_t zero = f2_pack(0.0f, 0.0f), one = f2_pack(1.0f, 1.0f), minus = f2_pack(-1.0f, -1.0f);
     {
         auto param = [&](const float *p, int i, int stride, int at) {
             return live && p && i < V ? p[static_cast<long long>(c + i) * stride + at] : 0.0f;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
                     f2_unpack(f2_mul(v, f2_pack(-kLog2e, -kLog2e)), e0, e1);
                     f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), one), q0, q1);
                     const f2_t s = f2_pack(rcp_approx(q0), rcp_approx(q1));
-                    const f2_t f = f2_mul(s, f2_fma(v, f2_sub(one, s), one));
+                    const f2_t f = f2_mul(s, f2_fma(v, f2_fma(s, minus, one), one));
                     dv[H][p] = f2_mul(g[p], f);
                     if (EDGE && tj >= L)
                         dv[H][p] = zero;

@@ -28,9 +28,8 @@
 //  * above that: the _wide kernels, which read a row more than once.
 //
 // Vectors of 4 elements where the rows begin on one, else single elements:
-// rows of an odd width start anywhere, so the copies into shared memory are
-// made of 16-byte pieces that are aligned in global memory and keep the row's
-// place in them.
+// rows of an odd width start anywhere, and the copies into shared memory keep
+// their place within 16 bytes.
 #pragma once
 
 #include <type_traits>
@@ -157,9 +156,9 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             f2_t m[2];
-            quad_where<V>(mean, col(j), 32, W, m);
-            v[j][0] = f2_sub(v[j][0], m[0]);
-            v[j][1] = f2_sub(v[j][1], m[1]);
+            quad_where<V>(-mean, col(j), 32, W, m);
+            v[j][0] = f2_add(v[j][0], m[0]);
+            v[j][1] = f2_add(v[j][1], m[1]);
             t0 = f2_fma(v[j][0], v[j][0], t0);
             t1 = f2_fma(v[j][1], v[j][1], t1);
         }
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         fetch(row);
     for (; row < a.rows; row += step) {
         f2_t h[NQ][2], g[NQ][2], s0 = f2_both(0.0f), s1 = s0;
-        const f2_t m = f2_both(mean), q = f2_both(rstd);
+        const f2_t m = f2_both(-mean), q = f2_both(rstd);
         const float rq = rstd;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 // elements behind the row have g = 0 and add nothing
-                h[j][i] = f2_mul(f2_sub(h[j][i], m), q);
+                h[j][i] = f2_mul(f2_add(h[j][i], m), q);
                 dw[j][i] = f2_fma(g[j][i], h[j][i], dw[j][i]);
                 db[j][i] = f2_add(db[j][i], g[j][i]);
                 g[j][i] = f2_mul(g[j][i], wv[j][i]);
@@ -360,18 +359,11 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 }
 
 // ------------------------------------------------ rows in shared memory
-// A copied row's buffer, as this thread's quads see it.  A row of an odd width
-// does not begin on a 16-byte boundary; the pieces around it that also hold the
-// neighbouring rows' bytes are read, never used.
-template <typename T>
-__device__ __forceinline__ const T *row_in(const unsigned char *buf, const T *tensor, long long at) {
-    return reinterpret_cast<const T *>(buf + in16(tensor, at));
-}
-
-// Forward: kNormStages rows of each warp in flight or in use; the copies of a
-// row are the lanes' own, so a warp waits for nothing but them.  w and b are
-// kept beside the rows.  Three passes over the row's buffer (sum, squared
-// deviations, output).
+// Rows come by bulk copies, a few tiles ahead of their use (kNormStages).
+// Forward, a row is a warp's own: lane 0 starts its copies and the warp waits
+// for them alone.  w and b are kept beside the rows.  Three passes over the
+// row's buffer (sum, squared deviations, output), each in the same order wherever
+// the row begins, so a row's result does not depend on its place.
 constexpr int kNormStages = 2;
 constexpr int kNormRowWarps = 8;  // warps of a block, or as many as shared memory allows
 
@@ -387,6 +379,7 @@ __global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kern
     using QF = Quad<float, V>;
     const NormFwdArgs &a = args.n;
     extern __shared__ __align__(16) unsigned char s6_norm_smem[];
+    __shared__ uint64_t full[kNormRowWarps][kNormStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int W = a.width, c0 = lane * V;
     const int whole = W & ~127;  // columns of whole steps of the warp: a quad a lane
@@ -395,31 +388,49 @@ __global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kern
     unsigned char *rows = reinterpret_cast<unsigned char *>(b + (W + 3) / 4 * 4) + warp * kNormStages * stage;
     const X *x = static_cast<const X *>(a.x);
     const Y *r = static_cast<const Y *>(a.r);
+    const long long total = a.rows * W;
 
     const long long step = static_cast<long long>(warps) * gridDim.x;
     long long row = static_cast<long long>(warps) * blockIdx.x + warp;
-    auto fetch = [&](int st, long long at) {
-        if (at < a.rows) {
-            row_copy(rows + st * stage, x + at * W, W, x, lane, 32);
-            if (r)
-                row_copy(rows + st * stage + args.x_bytes, r + at * W, W, r, lane, 32);
-        }
-        cp_async_commit();
+    auto fetch = [&](int st, long long at) {  // lane 0
+        unsigned char *to = rows + st * stage;
+        const BulkSpan sx = bulk_span(to, x, total, at * W, W);
+        BulkSpan sr{nullptr, 0, 0};
+        if (r)
+            sr = bulk_span(to + args.x_bytes, r, total, at * W, W);
+        mbar_arrive_expect_tx(&full[warp][st], sx.bytes + sr.bytes);
+        bulk_start(to, sx, &full[warp][st]);
+        bulk_start(to + args.x_bytes, sr, &full[warp][st]);
     };
-#pragma unroll
-    for (int st = 0; st < kNormStages; ++st)
-        fetch(st, row + st * step);
+    if (lane == 0) {
+        for (int st = 0; st < kNormStages; ++st)
+            mbar_init(&full[warp][st], 1);
+        fence_mbarrier_init();
+        for (int st = 0; st < kNormStages; ++st)
+            if (row + st * step < a.rows)
+                fetch(st, row + st * step);
+    }
     for (int c = threadIdx.x; c < W; c += blockDim.x) {
         w[c] = a.w ? a.w[c] : 1.0f;
         b[c] = a.b ? a.b[c] : 0.0f;
     }
     __syncthreads();
 
-    for (int st = 0; row < a.rows; row += step, st = st + 1 == kNormStages ? 0 : st + 1) {
-        cp_async_wait<kNormStages - 1>();
-        __syncwarp();
-        const X *xs = row_in(rows + st * stage, x, row * W);
-        const Y *rs = r ? row_in(rows + st * stage + args.x_bytes, r, row * W) : nullptr;
+    int st = 0;
+    uint32_t phase = 0;
+    for (; row < a.rows; row += step) {
+        const bool ok = mbar_wait_bounded(&full[warp][st], phase, kBulkPolls);
+        if (__any_sync(0xffffffffu, !ok)) {
+            if (lane == 0) {
+                raise_device_error(kErrTrainCopy);
+                // the copies still in flight are waited for, with the same bound
+                if (row + step < a.rows)
+                    mbar_wait_bounded(&full[warp][st ^ 1], st ? phase ^ 1u : phase, kBulkPolls);
+            }
+            return;
+        }
+        const X *xs = reinterpret_cast<const X *>(rows + st * stage + in16(x, row * W));
+        const Y *rs = r ? reinterpret_cast<const Y *>(rows + st * stage + args.x_bytes + in16(r, row * W)) : nullptr;
         auto value = [&](auto all, int c, f2_t (&v)[2]) {
             constexpr bool ALL = decltype(all)::value;
             QX q;
@@ -450,14 +461,15 @@ __global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kern
             t1 = f2_add(t1, v[1]);
         });
         const float mean = warp_sum(f2_sum(t0, t1)) * a.inv_w;
+        const f2_t m = f2_both(-mean);
         t0 = t1 = f2_both(0.0f);
         walk([&](auto all, int c) {
-            f2_t v[2], m[2] = {f2_both(mean), f2_both(mean)};
+            f2_t v[2], d[2] = {m, m};
             value(all, c, v);
             if constexpr (!decltype(all)::value)
-                quad_where<V>(mean, c, 32, W, m);
-            v[0] = f2_sub(v[0], m[0]);
-            v[1] = f2_sub(v[1], m[1]);
+                quad_where<V>(-mean, c, 32, W, d);
+            v[0] = f2_add(v[0], d[0]);
+            v[1] = f2_add(v[1], d[1]);
             t0 = f2_fma(v[0], v[0], t0);
             t1 = f2_fma(v[1], v[1], t1);
         });
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kern
         }
         X *sp = a.s ? static_cast<X *>(a.s) + row * W : nullptr;
         Y *yp = static_cast<Y *>(a.y) + row * W;
-        const f2_t m = f2_both(mean), q = f2_both(rstd);
+        const f2_t q = f2_both(rstd);
         walk([&](auto all, int c) {
             constexpr bool ALL = decltype(all)::value;
             f2_t v[2], wv[2], bv[2];
@@ -482,25 +494,31 @@ __global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kern
             p.pairs(wv);
             p.template load<ALL>(b, c, 32, W);
             p.pairs(bv);
-            const f2_t o[2] = {f2_fma(f2_mul(f2_sub(v[0], m), q), wv[0], bv[0]),
-                               f2_fma(f2_mul(f2_sub(v[1], m), q), wv[1], bv[1])};
+            const f2_t o[2] = {f2_fma(f2_mul(f2_add(v[0], m), q), wv[0], bv[0]),
+                               f2_fma(f2_mul(f2_add(v[1], m), q), wv[1], bv[1])};
             QY::template store<ALL>(yp, c, 32, W, o);
         });
         __syncwarp();  // every lane is done with the stage
-        fetch(st, row + kNormStages * step);
+        if (lane == 0 && row + kNormStages * step < a.rows)
+            fetch(st, row + kNormStages * step);
+        if (++st == kNormStages) {
+            st = 0;
+            phase ^= 1u;
+        }
     }
 }
 
-// Backward: a block takes `tile` rows at a time, kNormStages tiles in flight or
-// in use.  Each row's two sums are made by blockDim / 32 / tile warps, whose
-// parts every thread then adds in order; a thread owns NQ quads of columns and
-// keeps their dw and db in registers until the block's last tile.  Blocks have a
-// multiple of 4 warps, one for each scheduler of the SM: with 5 (which a width
-// of 2560 would fill exactly) the busiest one had 1.3 times its share.
+// Backward: a block takes `tile` consecutive rows at a time, which are one
+// stretch of each tensor; thread 0 starts their copies.  Each row's two sums are
+// made by blockDim / 32 / tile warps, whose parts every thread then adds in
+// order; a thread owns NQ quads of columns and keeps their dw and db in
+// registers until the block's last tile.  Blocks have a multiple of 4 warps,
+// one for each scheduler of the SM: with 5 (which a width of 2560 would fill
+// exactly) the busiest one had 1.3 times its share.
 struct NormTileArgs {
     NormBwdArgs n;
     int tile;
-    int x_bytes, dy_bytes, ds_bytes;  // row buffers
+    int x_bytes, dy_bytes, ds_bytes;  // a tile's buffers
 };
 
 constexpr int kNormTileRows = 8;  // at most
@@ -512,33 +530,42 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
     using QF = Quad<float, V>;
     const NormBwdArgs &a = args.n;
     extern __shared__ __align__(16) unsigned char s6_norm_smem[];
+    __shared__ uint64_t full[kNormStages];
     __shared__ float stats[kNormStages][kNormTileRows][2];  // mean, rstd
     __shared__ float2 parts[kNormTileRows][MAXT / 32];      // each warp's two sums
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int W = a.width, T = blockDim.x, R = args.tile;
-    const int share = warps / R;  // warps that sum a row
+    constexpr int T = MAXT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int W = a.width, R = args.tile;
+    const int share = T / 32 / R;  // warps that sum a row
     float *w = reinterpret_cast<float *>(s6_norm_smem);
-    const int rb = args.x_bytes + args.dy_bytes + args.ds_bytes;
+    const int stage = args.x_bytes + args.dy_bytes + args.ds_bytes;
     unsigned char *buf = reinterpret_cast<unsigned char *>(w + (W + 3) / 4 * 4);
     const X *x = static_cast<const X *>(a.x);
     const Y *dy = static_cast<const Y *>(a.dy);
+    const long long total = a.rows * W;
     auto col = [&](int j) { return static_cast<int>(threadIdx.x) * V + 4 * T * j; };
 
     const long long tiles = (a.rows + R - 1) / R;
+    auto rows_of = [&](long long tile) {
+        return a.rows - tile * R < R ? static_cast<int>(a.rows - tile * R) : R;
+    };
     auto fetch = [&](int st, long long tile) {
         if (tile < tiles) {
-            for (int k = 0; k < R; ++k) {
-                const long long row = tile * R + k;
-                if (row >= a.rows)
-                    break;
-                unsigned char *to = buf + (st * R + k) * rb;
-                row_copy(to, x + row * W, W, x, threadIdx.x, T);
-                row_copy(to + args.x_bytes, dy + row * W, W, dy, threadIdx.x, T);
+            const int n = rows_of(tile);
+            if (threadIdx.x == 0) {
+                unsigned char *to = buf + st * stage, *to_dy = to + args.x_bytes, *to_ds = to_dy + args.dy_bytes;
+                const long long at = tile * R * W, len = static_cast<long long>(n) * W;
+                const BulkSpan sx = bulk_span(to, x, total, at, len), sy = bulk_span(to_dy, dy, total, at, len);
+                BulkSpan se{nullptr, 0, 0};
                 if (a.ds)
-                    row_copy(to + args.x_bytes + args.dy_bytes, a.ds + row * W, W, a.ds, threadIdx.x, T);
+                    se = bulk_span(to_ds, a.ds, total, at, len);
+                mbar_arrive_expect_tx(&full[st], sx.bytes + sy.bytes + se.bytes);
+                bulk_start(to, sx, &full[st]);
+                bulk_start(to_dy, sy, &full[st]);
+                bulk_start(to_ds, se, &full[st]);
             }
             const int k = threadIdx.x;
-            if (k < R && tile * R + k < a.rows) {
+            if (k < n) {
                 cp_async4(&stats[st][k][0], a.mean + tile * R + k);
                 cp_async4(&stats[st][k][1], a.rstd + tile * R + k);
             }
@@ -546,6 +573,12 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
         cp_async_commit();
     };
     long long tile = blockIdx.x;
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < kNormStages; ++st)
+            mbar_init(&full[st], 1);
+        fence_mbarrier_init();
+    }
+    __syncthreads();
 #pragma unroll
     for (int st = 0; st < kNormStages; ++st)
         fetch(st, tile + static_cast<long long>(st) * gridDim.x);
@@ -558,17 +591,30 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
         dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = f2_both(0.0f);
     }
 
-    for (int st = 0; tile < tiles; tile += gridDim.x, st = st + 1 == kNormStages ? 0 : st + 1) {
-        const int here = a.rows - tile * R < R ? static_cast<int>(a.rows - tile * R) : R;
+    int st = 0;
+    uint32_t phase = 0;
+    for (; tile < tiles; tile += gridDim.x) {
+        const int here = rows_of(tile);
         cp_async_wait<kNormStages - 1>();
-        __syncthreads();
-        const unsigned char *rows = buf + st * R * rb;
+        const bool ok = mbar_wait_bounded(&full[st], phase, kBulkPolls);
+        if (__syncthreads_or(!ok)) {
+            if (threadIdx.x == 0) {
+                raise_device_error(kErrTrainCopy);
+                // the copies still in flight are waited for, with the same bound
+                if (tile + gridDim.x < tiles)
+                    mbar_wait_bounded(&full[st ^ 1], st ? phase ^ 1u : phase, kBulkPolls);
+            }
+            return;
+        }
+        const X *xs = reinterpret_cast<const X *>(buf + st * stage + in16(x, tile * R * W));
+        const Y *gs = reinterpret_cast<const Y *>(buf + st * stage + args.x_bytes + in16(dy, tile * R * W));
+        const float *es = reinterpret_cast<const float *>(buf + st * stage + args.x_bytes + args.dy_bytes +
+                                                          in16(a.ds, tile * R * W));
         if (warp / share < here) {
             const int k = warp / share, part = warp - k * share;
-            const long long at = (tile * R + k) * W;
-            const X *xs = row_in(rows + k * rb, x, at);
-            const Y *gs = row_in(rows + k * rb + args.x_bytes, dy, at);
-            const f2_t m = f2_both(stats[st][k][0]), q = f2_both(stats[st][k][1]);
+            const X *xk = xs + k * W;
+            const Y *gk = gs + k * W;
+            const f2_t m = f2_both(-stats[st][k][0]), q = f2_both(stats[st][k][1]);
             f2_t s0 = f2_both(0.0f), s1 = s0;
             auto one = [&](auto all, int c) {
                 constexpr bool ALL = decltype(all)::value;
@@ -576,8 +622,8 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
                 QY gq;
                 QF wq;
                 f2_t h[2], g[2], wc[2];
-                xq.template load<ALL>(xs, c, 32, W);
-                gq.template load<ALL>(gs, c, 32, W);
+                xq.template load<ALL>(xk, c, 32, W);
+                gq.template load<ALL>(gk, c, 32, W);
                 wq.template load<ALL>(w, c, 32, W);
                 xq.pairs(h);
                 gq.pairs(g);
@@ -586,7 +632,7 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
                 for (int i = 0; i < 2; ++i) {
                     g[i] = f2_mul(g[i], wc[i]);
                     s0 = f2_add(s0, g[i]);
-                    s1 = f2_fma(g[i], f2_mul(f2_sub(h[i], m), q), s1);
+                    s1 = f2_fma(g[i], f2_mul(f2_add(h[i], m), q), s1);
                 }
             };
             int c = part * 128;
@@ -606,15 +652,11 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
         }
         __syncthreads();
         float *dxp = a.dx + tile * R * W;
-        for (int k = 0; k < here; ++k, dxp += W) {
-            const long long at = (tile * R + k) * W;
-            const X *xs = row_in(rows + k * rb, x, at);
-            const Y *gs = row_in(rows + k * rb + args.x_bytes, dy, at);
-            const float *es = row_in(rows + k * rb + args.x_bytes + args.dy_bytes, a.ds, at);
+        for (int k = 0; k < here; ++k, dxp += W, xs += W, gs += W, es += W) {
             const float rstd = stats[st][k][1];
-            const f2_t m = f2_both(stats[st][k][0]), q = f2_both(rstd);
-            float m0 = 0.0f, m1 = 0.0f;
-            for (int p = 0; p < share; ++p) {
+            const f2_t m = f2_both(-stats[st][k][0]), q = f2_both(rstd);
+            float m0 = parts[k][0].x, m1 = parts[k][0].y;
+            for (int p = 1; p < share; ++p) {
                 m0 += parts[k][p].x;
                 m1 += parts[k][p].y;
             }
@@ -630,7 +672,7 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
                 gq.pairs(g);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    h[i] = f2_mul(f2_sub(h[i], m), q);
+                    h[i] = f2_mul(f2_add(h[i], m), q);
                     dw[j][i] = f2_fma(g[i], h[i], dw[j][i]);
                     db[j][i] = f2_add(db[j][i], g[i]);
                     o[i] = f2_fma(f2_fma(h[i], c1, f2_mul(g[i], wv[j][i])), q, c0);
@@ -655,6 +697,10 @@ __global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const
         }
         __syncthreads();  // every thread is done with the stage
         fetch(st, tile + static_cast<long long>(kNormStages) * gridDim.x);
+        if (++st == kNormStages) {
+            st = 0;
+            phase ^= 1u;
+        }
     }
     if (!a.part)
         return;

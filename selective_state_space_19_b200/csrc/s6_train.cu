@@ -125,24 +125,35 @@ NormPlan norm_rows_plan(int64_t rows, int64_t width, int64_t row_bytes) {
 }
 
 // Backward through shared memory: 4, 8 or 16 warps with as many quads of columns a
-// thread as hold the row; then the most rows of a tile that leave room for the
-// blocks that the registers allow on an SM.
-NormPlan norm_tile_plan(int64_t rows, int64_t width, int64_t row_bytes) {
+// thread as hold the row (up to 5, 5 and 4); then the most rows of a tile that
+// leave room for the blocks that the registers allow on an SM.
+template <typename Bytes>
+NormPlan norm_tile_plan(int64_t rows, int64_t width, Bytes tile_bytes) {
     NormPlan p;
     const int64_t quads = ceil_div(width, 128);  // of a warp
-    const int64_t warps = quads <= 16 ? 4 : quads <= 32 ? 8 : 16;
+    const int64_t warps = quads <= 20 ? 4 : quads <= 40 ? 8 : 16;
     p.elems = static_cast<int>(4 * ceil_div(quads, warps));
     const int64_t fixed = norm_params_bytes(width), most = norm_tile_resident(warps);
     const int64_t statics = 2 * kSmemBlock;  // the kernel's own shared arrays and the system's part
     int64_t tile = std::min<int64_t>(s6::kNormTileRows, warps);
-    while (tile > 1 && fixed + s6::kNormStages * tile * row_bytes > kSmemSM / std::min<int64_t>(most, 3) - statics)
+    while (tile > 1 && fixed + s6::kNormStages * tile_bytes(tile) > kSmemSM / most - statics)
         tile /= 2;
     p.tile = static_cast<int>(tile);
     p.threads = static_cast<int>(32 * warps);
-    p.smem = fixed + s6::kNormStages * tile * row_bytes;
+    p.smem = fixed + s6::kNormStages * tile_bytes(tile);
     p.blocks = std::min(ceil_div(rows, tile), kSMs * std::min(blocks_of_smem(p.smem + kSmemBlock), most));
     return p;
 }
+
+// A tile's buffers: x, dy and, where it is given, ds.
+struct NormTileBytes {
+    int64_t width, sx, sy;
+    bool ds;
+    int64_t x(int64_t tile) const { return s6::row_buffer_bytes(tile * width * sx); }
+    int64_t dy(int64_t tile) const { return s6::row_buffer_bytes(tile * width * sy); }
+    int64_t e(int64_t tile) const { return ds ? s6::row_buffer_bytes(tile * width * 4) : 0; }
+    int64_t operator()(int64_t tile) const { return x(tile) + dy(tile) + e(tile); }
+};
 
 // Runs of rows of the wide backward's second kernel: enough blocks to fill the
 // SMs at its 128-thread blocks, whatever the vector width.
@@ -204,21 +215,25 @@ int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
                        norm_rows_plan(a.rows, a.width, r.x_bytes + r.r_bytes), st, r);
 }
 
-// Quads of a thread and threads of a block: 2 to 4 with 4 warps (widths up to 2048),
-// 3 or 4 with 8 and with 16.
+// Quads of a thread and threads of a block: 2 to 5 with 4 warps, 3 to 5 with 8, 3 or 4
+// with 16.
 template <typename X, typename Y, int V, int NQ, int T>
 int norm_tile_t(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
     return launch_smem(s6::s6_layernorm_bwd_tile_kernel<X, Y, V, NQ, T, norm_tile_resident(T / 32)>, p, st, a);
 }
 template <typename X, typename Y, int V>
 int norm_tile(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
+    const int nq = p.elems / 4;
     if (p.threads == 128)
-        return p.elems <= 8    ? norm_tile_t<X, Y, V, 2, 128>(a, p, st)
-               : p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 128>(a, p, st)
-                               : norm_tile_t<X, Y, V, 4, 128>(a, p, st);
+        return nq <= 2   ? norm_tile_t<X, Y, V, 2, 128>(a, p, st)
+               : nq == 3 ? norm_tile_t<X, Y, V, 3, 128>(a, p, st)
+               : nq == 4 ? norm_tile_t<X, Y, V, 4, 128>(a, p, st)
+                         : norm_tile_t<X, Y, V, 5, 128>(a, p, st);
     if (p.threads == 256)
-        return p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 256>(a, p, st) : norm_tile_t<X, Y, V, 4, 256>(a, p, st);
-    return p.elems <= 12 ? norm_tile_t<X, Y, V, 3, 512>(a, p, st) : norm_tile_t<X, Y, V, 4, 512>(a, p, st);
+        return nq <= 3   ? norm_tile_t<X, Y, V, 3, 256>(a, p, st)
+               : nq == 4 ? norm_tile_t<X, Y, V, 4, 256>(a, p, st)
+                         : norm_tile_t<X, Y, V, 5, 256>(a, p, st);
+    return nq <= 3 ? norm_tile_t<X, Y, V, 3, 512>(a, p, st) : norm_tile_t<X, Y, V, 4, 512>(a, p, st);
 }
 
 template <typename X, typename Y, int V>
@@ -248,12 +263,13 @@ int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db,
         } else {
             s6::NormTileArgs t;
             t.n = a;
-            t.x_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(X)));
-            t.dy_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(Y)));
-            t.ds_bytes = a.ds ? s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(float))) : 0;
-            const NormPlan p = norm_tile_plan(a.rows, a.width, t.x_bytes + t.dy_bytes + t.ds_bytes);
+            const NormTileBytes bytes{a.width, sizeof(X), sizeof(Y), a.ds != nullptr};
+            const NormPlan p = norm_tile_plan(a.rows, a.width, bytes);
             parts = p.blocks;
             t.tile = p.tile;
+            t.x_bytes = static_cast<int>(bytes.x(p.tile));
+            t.dy_bytes = static_cast<int>(bytes.dy(p.tile));
+            t.ds_bytes = static_cast<int>(bytes.e(p.tile));
             rc = norm_tile<X, Y, V>(t, p, st);
         }
         if (rc != S6_OK)
@@ -491,6 +507,10 @@ int grads_common(int64_t count, const void *const *grads, const int64_t *numel, 
 
 }  // namespace
 
+// The error word of this translation unit's kernels (s6_device_status reads it
+// beside that of s6_abi.cu).
+cudaError_t s6_train_error_word(void **word) { return cudaGetSymbolAddress(word, s6::g_s6_device_error); }
+
 extern "C" {
 
 int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void *r, const float *w, const float *b, void *s,
@@ -542,11 +562,12 @@ int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims) {
     if (dims->width <= s6::kNormWarpWidth)
         return norm_warp_plan(dims->rows, dims->width, true).blocks * row;
     // with or without ds: the smaller rows may give more blocks, or the larger ones (shorter tiles)
-    const int64_t io = s6::row_buffer_bytes(dims->width * static_cast<int64_t>(io_size(dims->x_dtype))) +
-                       s6::row_buffer_bytes(dims->width * static_cast<int64_t>(io_size(dims->y_dtype)));
-    const int64_t ds = s6::row_buffer_bytes(dims->width * static_cast<int64_t>(sizeof(float)));
-    return row * std::max(norm_tile_plan(dims->rows, dims->width, io).blocks,
-                          norm_tile_plan(dims->rows, dims->width, io + ds).blocks);
+    NormTileBytes bytes{dims->width, static_cast<int64_t>(io_size(dims->x_dtype)),
+                        static_cast<int64_t>(io_size(dims->y_dtype)), false};
+    int64_t blocks = norm_tile_plan(dims->rows, dims->width, bytes).blocks;
+    bytes.ds = true;
+    blocks = std::max(blocks, norm_tile_plan(dims->rows, dims->width, bytes).blocks);
+    return blocks * row;
 }
 
 int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd, const float *w,

@@ -135,12 +135,6 @@ __device__ __forceinline__ float f2_sum(f2_t a, f2_t b) {
 }
 
 // ------------------------------------------------- rows into shared memory
-// 16-byte asynchronous copy of the first `bytes` (1 .. 16) at src; the rest of
-// dst reads as zero.  Both addresses 16-byte aligned.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
-                 : "memory");
-}
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -150,7 +144,7 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shared bytes that a row of n bytes may take: it keeps its place within 16 bytes.
+// Shared bytes that rows of n bytes in all may take: they keep their place within 16 bytes.
 __host__ __device__ constexpr int row_buffer_bytes(long long n) { return static_cast<int>((n + 15) / 16 * 16 + 16); }
 
 // The place of an address within 16 bytes; that of element `at` of a tensor.
@@ -161,25 +155,48 @@ __device__ __forceinline__ int in16(const T *p, long long at) {
                              static_cast<uint32_t>(at) * static_cast<uint32_t>(sizeof(T))) & 15u);
 }
 
-// Starts copying the n elements at src into buf, src's place within 16 bytes
-// kept (element 0 lands at buf + in16(src)), by `threads` threads of index t.
-// The copies begin on a 16-byte boundary, so up to 15 bytes in front of the row
-// come along: the end of the row before it, or, where the tensor itself (at
-// `tensor`) begins off the boundary, nothing: that one copy is made of elements.
+// A stretch of a tensor to be copied into shared memory by one bulk copy, which
+// must begin and end on 16-byte boundaries of global memory: the stretch keeps
+// its place within 16 bytes, and the up to 15 bytes around it that the copy
+// brings along are its neighbours in the tensor.  Where the tensor itself begins
+// or ends off a boundary, the copy stays inside it and the few elements between
+// are moved singly.
+struct BulkSpan {
+    const unsigned char *from;
+    uint32_t at, bytes;  // place of the copy in the buffer, and its size (0: none)
+};
+
+// Elements [first, first + n) of the `total` at `tensor` into buf (element
+// `first` lands at buf + in16 of its address); moves the single elements.
 template <typename T>
-__device__ __forceinline__ void row_copy(unsigned char *buf, const T *src, int n, const void *tensor, int t,
-                                         int threads) {
-    const int at = in16(src), total = at + n * static_cast<int>(sizeof(T));
-    const unsigned char *from = reinterpret_cast<const unsigned char *>(src) - at;
-    for (int k = t * 16; k < total; k += threads * 16) {
-        if (k > 0 || from >= static_cast<const unsigned char *>(tensor)) {
-            cp_async16(buf + k, from + k, total - k < 16 ? total - k : 16);
-        } else {
-            for (int i = at; i < 16 && i < total; i += sizeof(T))
-                *reinterpret_cast<T *>(buf + i) = *reinterpret_cast<const T *>(from + i);
-        }
-    }
+__device__ __forceinline__ BulkSpan bulk_span(unsigned char *buf, const T *tensor, long long total, long long first,
+                                              long long n) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(tensor), end = begin + total * sizeof(T);
+    const uintptr_t a = begin + first * sizeof(T), b = a + n * sizeof(T), base = a & ~static_cast<uintptr_t>(15);
+    uintptr_t lo = base, hi = (b + 15) & ~static_cast<uintptr_t>(15);
+    if (lo < begin)
+        lo += 16;
+    if (hi > end)
+        hi -= 16;
+    if (hi <= lo)
+        lo = hi = b;  // all of it singly
+    for (uintptr_t p = a; p < lo; p += sizeof(T))
+        *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
+    for (uintptr_t p = hi > a ? hi : a; p < b; p += sizeof(T))
+        *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
+    BulkSpan s;
+    s.from = reinterpret_cast<const unsigned char *>(lo);
+    s.at = static_cast<uint32_t>(lo - base);
+    s.bytes = static_cast<uint32_t>(hi - lo);
+    return s;
 }
+__device__ __forceinline__ void bulk_start(unsigned char *buf, const BulkSpan &s, uint64_t *bar) {
+    if (s.bytes)
+        bulk_load(buf + s.at, s.from, s.bytes, bar);
+}
+
+constexpr uint32_t kBulkPolls = 1u << 22;  // bound of a wait for a copy, far above any that arrives
+constexpr unsigned int kErrTrainCopy = 16u;  // bit of the device error word: such a wait gave up
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
