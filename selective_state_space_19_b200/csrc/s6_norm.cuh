@@ -19,12 +19,8 @@
 //  * up to kNormWarpWidth: a row is one warp's, in its registers.  The warp
 //    walks rows with a fixed stride and fetches the next one while it reduces
 //    the present one.
-//  * up to kNormMaxWidth: rows pass through shared memory, copied ahead of
-//    their use without registers.  Forward, a row is one warp's still, so it
-//    needs no barrier; backward, a block takes some rows at a time, a few
-//    warps sum each row, and then each thread does its own columns of all of
-//    them.  (Rows split over a block's registers, which this replaces, spent
-//    44 instructions an element on reductions and addresses at a width of 2560.)
+//  * up to kNormMaxWidth: rows come through shared memory, copied ahead of
+//    their use without registers, and a block takes two of them at a time.
 //  * above that: the _wide kernels, which read a row more than once.
 //
 // Vectors of 4 elements where the rows begin on one, else single elements:
@@ -359,348 +355,331 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 }
 
 // ------------------------------------------------ rows in shared memory
-// Rows come by bulk copies, a few tiles ahead of their use (kNormStages).
-// Forward, a row is a warp's own: lane 0 starts its copies and the warp waits
-// for them alone.  w and b are kept beside the rows.  Three passes over the
-// row's buffer (sum, squared deviations, output), each in the same order wherever
-// the row begins, so a row's result does not depend on its place.
-constexpr int kNormStages = 2;
-constexpr int kNormRowWarps = 8;  // warps of a block, or as many as shared memory allows
+// A block of T threads takes R consecutive rows (one stretch of each tensor) at
+// a step.  They come by bulk copies that thread 0 starts `stages` - 1 steps
+// ahead; each thread takes NQ quads of columns of every row into registers once
+// and keeps its columns' parameters (and, backward, their gradients' sums) in
+// registers over all steps.  Two rows a step share the reductions' shuffles and
+// barriers, which with one row, or with rows that pass through registers alone,
+// cost more than the arithmetic (44 instructions an element at a width of 2560;
+// rows summed by a warp each and read again for the output took 30).  Blocks
+// have a multiple of 4 warps, one for each scheduler of the SM: with 5, the
+// busiest scheduler had 1.3 times its share.
+constexpr int kNormMaxStages = 4;
 
-struct NormRowsArgs {
-    NormFwdArgs n;
-    int x_bytes, r_bytes;  // row buffers
+struct NormStream {
+    int stages;
+    int x_bytes, y_bytes, e_bytes;  // a step's buffers: x; r or dy; ds
+    int stage() const { return x_bytes + y_bytes + e_bytes; }
 };
 
-template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(32 * kNormRowWarps) s6_layernorm_fwd_rows_kernel(const NormRowsArgs args) {
-    using QX = Quad<X, V>;
-    using QY = Quad<Y, V>;
-    using QF = Quad<float, V>;
-    const NormFwdArgs &a = args.n;
-    extern __shared__ __align__(16) unsigned char s6_norm_smem[];
-    __shared__ uint64_t full[kNormRowWarps][kNormStages];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int W = a.width, c0 = lane * V;
-    const int whole = W & ~127;  // columns of whole steps of the warp: a quad a lane
-    float *w = reinterpret_cast<float *>(s6_norm_smem), *b = w + (W + 3) / 4 * 4;
-    const int stage = args.x_bytes + args.r_bytes;
-    unsigned char *rows = reinterpret_cast<unsigned char *>(b + (W + 3) / 4 * 4) + warp * kNormStages * stage;
-    const X *x = static_cast<const X *>(a.x);
-    const Y *r = static_cast<const Y *>(a.r);
-    const long long total = a.rows * W;
+// The ring of a block's steps.
+struct NormRing {
+    unsigned char *buf;
+    uint64_t *full;
+    int stages, stage_bytes;
+    int st;          // stage of the present step
+    uint32_t phase;  // its parity
 
-    const long long step = static_cast<long long>(warps) * gridDim.x;
-    long long row = static_cast<long long>(warps) * blockIdx.x + warp;
-    auto fetch = [&](int st, long long at) {  // lane 0
-        unsigned char *to = rows + st * stage;
-        const BulkSpan sx = bulk_span(to, x, total, at * W, W);
-        BulkSpan sr{nullptr, 0, 0};
-        if (r)
-            sr = bulk_span(to + args.x_bytes, r, total, at * W, W);
-        mbar_arrive_expect_tx(&full[warp][st], sx.bytes + sr.bytes);
-        bulk_start(to, sx, &full[warp][st]);
-        bulk_start(to + args.x_bytes, sr, &full[warp][st]);
-    };
-    if (lane == 0) {
-        for (int st = 0; st < kNormStages; ++st)
-            mbar_init(&full[warp][st], 1);
-        fence_mbarrier_init();
-        for (int st = 0; st < kNormStages; ++st)
-            if (row + st * step < a.rows)
-                fetch(st, row + st * step);
-    }
-    for (int c = threadIdx.x; c < W; c += blockDim.x) {
-        w[c] = a.w ? a.w[c] : 1.0f;
-        b[c] = a.b ? a.b[c] : 0.0f;
-    }
-    __syncthreads();
-
-    int st = 0;
-    uint32_t phase = 0;
-    for (; row < a.rows; row += step) {
-        const bool ok = mbar_wait_bounded(&full[warp][st], phase, kBulkPolls);
-        if (__any_sync(0xffffffffu, !ok)) {
-            if (lane == 0) {
-                raise_device_error(kErrTrainCopy);
-                // the copies still in flight are waited for, with the same bound
-                if (row + step < a.rows)
-                    mbar_wait_bounded(&full[warp][st ^ 1], st ? phase ^ 1u : phase, kBulkPolls);
-            }
-            return;
-        }
-        const X *xs = reinterpret_cast<const X *>(rows + st * stage + in16(x, row * W));
-        const Y *rs = r ? reinterpret_cast<const Y *>(rows + st * stage + args.x_bytes + in16(r, row * W)) : nullptr;
-        auto value = [&](auto all, int c, f2_t (&v)[2]) {
-            constexpr bool ALL = decltype(all)::value;
-            QX q;
-            q.template load<ALL>(xs, c, 32, W);
-            q.pairs(v);
-            if (r) {
-                QY p;
-                f2_t t[2];
-                p.template load<ALL>(rs, c, 32, W);
-                p.pairs(t);
-                v[0] = f2_add(v[0], t[0]);
-                v[1] = f2_add(v[1], t[1]);
-            }
-        };
-        // fn(all, column) for the whole steps, then for the one that the row's end cuts
-        auto walk = [&](auto fn) {
-#pragma unroll 4
-            for (int c = 0; c < whole; c += 128)
-                fn(std::true_type{}, c0 + c);
-            if (whole < W)
-                fn(std::false_type{}, c0 + whole);
-        };
-        f2_t t0 = f2_both(0.0f), t1 = t0;
-        walk([&](auto all, int c) {
-            f2_t v[2];
-            value(all, c, v);
-            t0 = f2_add(t0, v[0]);
-            t1 = f2_add(t1, v[1]);
-        });
-        const float mean = warp_sum(f2_sum(t0, t1)) * a.inv_w;
-        const f2_t m = f2_both(-mean);
-        t0 = t1 = f2_both(0.0f);
-        walk([&](auto all, int c) {
-            f2_t v[2], d[2] = {m, m};
-            value(all, c, v);
-            if constexpr (!decltype(all)::value)
-                quad_where<V>(-mean, c, 32, W, d);
-            v[0] = f2_add(v[0], d[0]);
-            v[1] = f2_add(v[1], d[1]);
-            t0 = f2_fma(v[0], v[0], t0);
-            t1 = f2_fma(v[1], v[1], t1);
-        });
-        const float rstd = __frsqrt_rn(warp_sum(f2_sum(t0, t1)) * a.inv_w + a.eps);
-        if (lane == 0) {
-            if (a.mean)
-                a.mean[row] = mean;
-            if (a.rstd)
-                a.rstd[row] = rstd;
-        }
-        X *sp = a.s ? static_cast<X *>(a.s) + row * W : nullptr;
-        Y *yp = static_cast<Y *>(a.y) + row * W;
-        const f2_t q = f2_both(rstd);
-        walk([&](auto all, int c) {
-            constexpr bool ALL = decltype(all)::value;
-            f2_t v[2], wv[2], bv[2];
-            value(all, c, v);
-            if (sp)
-                QX::template store<ALL>(sp, c, 32, W, v);
-            QF p;
-            p.template load<ALL>(w, c, 32, W);
-            p.pairs(wv);
-            p.template load<ALL>(b, c, 32, W);
-            p.pairs(bv);
-            const f2_t o[2] = {f2_fma(f2_mul(f2_add(v[0], m), q), wv[0], bv[0]),
-                               f2_fma(f2_mul(f2_add(v[1], m), q), wv[1], bv[1])};
-            QY::template store<ALL>(yp, c, 32, W, o);
-        });
-        __syncwarp();  // every lane is done with the stage
-        if (lane == 0 && row + kNormStages * step < a.rows)
-            fetch(st, row + kNormStages * step);
-        if (++st == kNormStages) {
+    __device__ __forceinline__ unsigned char *at() const { return buf + st * stage_bytes; }
+    __device__ __forceinline__ bool wait() const { return mbar_wait_bounded(&full[st], phase, kBulkPolls); }
+    __device__ __forceinline__ void next() {
+        if (++st == stages) {
             st = 0;
             phase ^= 1u;
         }
     }
-}
-
-// Backward: a block takes `tile` consecutive rows at a time, which are one
-// stretch of each tensor; thread 0 starts their copies.  Each row's two sums are
-// made by blockDim / 32 / tile warps, whose parts every thread then adds in
-// order; a thread owns NQ quads of columns and keeps their dw and db in
-// registers until the block's last tile.  Blocks have a multiple of 4 warps,
-// one for each scheduler of the SM: with 5 (which a width of 2560 would fill
-// exactly) the busiest one had 1.3 times its share.
-struct NormTileArgs {
-    NormBwdArgs n;
-    int tile;
-    int x_bytes, dy_bytes, ds_bytes;  // a tile's buffers
+    // After a wait that gave up: one thread waits, with the same bound, for the copies of
+    // the `left` steps behind the present one that have been started.
+    __device__ __forceinline__ void drain(int left) {
+        raise_device_error(kErrTrainCopy);
+        for (int k = 0; k < left; ++k) {
+            next();
+            wait();
+        }
+    }
 };
 
-constexpr int kNormTileRows = 8;  // at most
+struct NormFwdBlockArgs {
+    NormFwdArgs n;
+    NormStream s;
+};
 
-template <typename X, typename Y, int V, int NQ, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) s6_layernorm_bwd_tile_kernel(const NormTileArgs args) {
+template <typename X, typename Y, int V, int NQ, int R, int T, int MINB>
+__global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const NormFwdBlockArgs args) {
+    using QX = Quad<X, V>;
+    using QY = Quad<Y, V>;
+    constexpr int WARPS = T / 32;
+    const NormFwdArgs &a = args.n;
+    extern __shared__ __align__(16) unsigned char s6_norm_smem[];
+    __shared__ uint64_t full[kNormMaxStages];
+    __shared__ float slots[2][4][16];
+    const int tid = threadIdx.x, W = a.width;
+    const X *x = static_cast<const X *>(a.x);
+    const Y *r = static_cast<const Y *>(a.r);
+    auto col = [&](int j) { return tid * V + 4 * T * j; };
+    const long long steps = (a.rows + R - 1) / R, total = a.rows * W;
+    NormRing ring{s6_norm_smem, full, args.s.stages, args.s.x_bytes + args.s.y_bytes, 0, 0u};
+
+    auto fetch = [&](int st, long long step) {  // thread 0
+        const long long first = step * R * W;
+        const uint32_t n = static_cast<uint32_t>((a.rows - step * R < R ? a.rows - step * R : R) * W);
+        unsigned char *to = ring.buf + st * ring.stage_bytes;
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), r0 = reinterpret_cast<uintptr_t>(r);
+        bulk_fetch<X>(to, x0 + first * sizeof(X), n * sizeof(X), x0, x0 + total * sizeof(X), &full[st]);
+        if (r)
+            bulk_fetch<Y>(to + args.s.x_bytes, r0 + first * sizeof(Y), n * sizeof(Y), r0,
+                                   r0 + total * sizeof(Y), &full[st]);
+        mbar_arrive(&full[st]);
+    };
+    if (tid == 0) {
+        for (int st = 0; st < ring.stages; ++st)
+            mbar_init(&full[st], 1);
+        fence_mbarrier_init();
+        for (int st = 0; st < ring.stages; ++st)
+            if (blockIdx.x + static_cast<long long>(st) * gridDim.x < steps)
+                fetch(st, blockIdx.x + static_cast<long long>(st) * gridDim.x);
+    }
+    f2_t wv[NQ][2], bv[NQ][2];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        quad_params<V>(a.w, 1.0f, col(j), T, W, wv[j]);
+        quad_params<V>(a.b, 0.0f, col(j), T, W, bv[j]);
+    }
+    __syncthreads();
+
+    for (long long step = blockIdx.x; step < steps; step += gridDim.x) {
+        const long long row = step * R;
+        const int here = a.rows - row < R ? static_cast<int>(a.rows - row) : R;
+        const bool ok = ring.wait();
+        const X *xs = reinterpret_cast<const X *>(ring.at() + in16(x, row * W));
+        const Y *rs = reinterpret_cast<const Y *>(ring.at() + args.s.x_bytes + in16(r, row * W));
+        f2_t v[R][NQ][2];
+        float sum[R];
+        // a row that is not there is read as zeros
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int n = k < here ? W : 0;
+            f2_t t0 = f2_both(0.0f), t1 = t0;
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                QX q;
+                q.template load<false>(xs + k * W, col(j), T, n);
+                q.pairs(v[k][j]);
+                if (r) {
+                    QY p;
+                    f2_t t[2];
+                    p.template load<false>(rs + k * W, col(j), T, n);
+                    p.pairs(t);
+                    v[k][j][0] = f2_add(v[k][j][0], t[0]);
+                    v[k][j][1] = f2_add(v[k][j][1], t[1]);
+                    if (a.s)
+                        QX::template store<false>(static_cast<X *>(a.s) + (row + k) * W, col(j), T, n, v[k][j]);
+                }
+                t0 = f2_add(t0, v[k][j][0]);
+                t1 = f2_add(t1, v[k][j][1]);
+            }
+            sum[k] = f2_sum(t0, t1);
+        }
+        if (block_sums<R, WARPS>(sum, slots[0], !ok)) {
+            if (tid == 0) {
+                const long long more = (steps - 1 - step) / gridDim.x;
+                ring.drain(more < ring.stages - 1 ? static_cast<int>(more) : ring.stages - 1);
+            }
+            return;
+        }
+        // every thread has taken the step into registers: its stage is free
+        if (tid == 0 && step + static_cast<long long>(ring.stages) * gridDim.x < steps)
+            fetch(ring.st, step + static_cast<long long>(ring.stages) * gridDim.x);
+        ring.next();
+        float mean[R], sq[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] = sum[k] * a.inv_w;
+            f2_t t0 = f2_both(0.0f), t1 = t0;
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                f2_t m[2];
+                quad_where<V>(-mean[k], col(j), T, W, m);
+                v[k][j][0] = f2_add(v[k][j][0], m[0]);
+                v[k][j][1] = f2_add(v[k][j][1], m[1]);
+                t0 = f2_fma(v[k][j][0], v[k][j][0], t0);
+                t1 = f2_fma(v[k][j][1], v[k][j][1], t1);
+            }
+            sq[k] = f2_sum(t0, t1);
+        }
+        block_sums<R, WARPS>(sq, slots[1], false);
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (k < here) {
+                const float rstd = __frsqrt_rn(sq[k] * a.inv_w + a.eps);
+                if (tid == 0) {
+                    if (a.mean)
+                        a.mean[row + k] = mean[k];
+                    if (a.rstd)
+                        a.rstd[row + k] = rstd;
+                }
+                const f2_t q = f2_both(rstd);
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const f2_t o[2] = {f2_fma(f2_mul(v[k][j][0], q), wv[j][0], bv[j][0]),
+                                       f2_fma(f2_mul(v[k][j][1], q), wv[j][1], bv[j][1])};
+                    QY::template store<false>(static_cast<Y *>(a.y) + (row + k) * W, col(j), T, W, o);
+                }
+            }
+    }
+}
+
+struct NormBwdBlockArgs {
+    NormBwdArgs n;
+    NormStream s;
+};
+
+template <typename X, typename Y, int V, int NQ, int R, int T, int MINB>
+__global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const NormBwdBlockArgs args) {
     using QX = Quad<X, V>;
     using QY = Quad<Y, V>;
     using QF = Quad<float, V>;
+    constexpr int WARPS = T / 32;
     const NormBwdArgs &a = args.n;
     extern __shared__ __align__(16) unsigned char s6_norm_smem[];
-    __shared__ uint64_t full[kNormStages];
-    __shared__ float stats[kNormStages][kNormTileRows][2];  // mean, rstd
-    __shared__ float2 parts[kNormTileRows][MAXT / 32];      // each warp's two sums
-    constexpr int T = MAXT;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int W = a.width, R = args.tile;
-    const int share = T / 32 / R;  // warps that sum a row
-    float *w = reinterpret_cast<float *>(s6_norm_smem);
-    const int stage = args.x_bytes + args.dy_bytes + args.ds_bytes;
-    unsigned char *buf = reinterpret_cast<unsigned char *>(w + (W + 3) / 4 * 4);
+    __shared__ uint64_t full[kNormMaxStages];
+    __shared__ float slots[2][4][16];
+    const int tid = threadIdx.x, W = a.width;
     const X *x = static_cast<const X *>(a.x);
     const Y *dy = static_cast<const Y *>(a.dy);
-    const long long total = a.rows * W;
-    auto col = [&](int j) { return static_cast<int>(threadIdx.x) * V + 4 * T * j; };
+    auto col = [&](int j) { return tid * V + 4 * T * j; };
+    const long long steps = (a.rows + R - 1) / R, total = a.rows * W;
+    NormRing ring{s6_norm_smem, full, args.s.stages, args.s.x_bytes + args.s.y_bytes + args.s.e_bytes, 0, 0u};
 
-    const long long tiles = (a.rows + R - 1) / R;
-    auto rows_of = [&](long long tile) {
-        return a.rows - tile * R < R ? static_cast<int>(a.rows - tile * R) : R;
+    auto fetch = [&](int st, long long step) {  // thread 0
+        const long long first = step * R * W;
+        const uint32_t n = static_cast<uint32_t>((a.rows - step * R < R ? a.rows - step * R : R) * W);
+        unsigned char *to = ring.buf + st * ring.stage_bytes;
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), g0 = reinterpret_cast<uintptr_t>(dy),
+                        e0 = reinterpret_cast<uintptr_t>(a.ds);
+        bulk_fetch<X>(to, x0 + first * sizeof(X), n * sizeof(X), x0, x0 + total * sizeof(X), &full[st]);
+        bulk_fetch<Y>(to + args.s.x_bytes, g0 + first * sizeof(Y), n * sizeof(Y), g0, g0 + total * sizeof(Y),
+                               &full[st]);
+        if (a.ds)
+            bulk_fetch<float>(to + args.s.x_bytes + args.s.y_bytes, e0 + first * 4, n * 4, e0, e0 + total * 4,
+                                       &full[st]);
+        mbar_arrive(&full[st]);
     };
-    auto fetch = [&](int st, long long tile) {
-        if (tile < tiles) {
-            const int n = rows_of(tile);
-            if (threadIdx.x == 0) {
-                unsigned char *to = buf + st * stage, *to_dy = to + args.x_bytes, *to_ds = to_dy + args.dy_bytes;
-                const long long at = tile * R * W, len = static_cast<long long>(n) * W;
-                const BulkSpan sx = bulk_span(to, x, total, at, len), sy = bulk_span(to_dy, dy, total, at, len);
-                BulkSpan se{nullptr, 0, 0};
-                if (a.ds)
-                    se = bulk_span(to_ds, a.ds, total, at, len);
-                mbar_arrive_expect_tx(&full[st], sx.bytes + sy.bytes + se.bytes);
-                bulk_start(to, sx, &full[st]);
-                bulk_start(to_dy, sy, &full[st]);
-                bulk_start(to_ds, se, &full[st]);
-            }
-            const int k = threadIdx.x;
-            if (k < n) {
-                cp_async4(&stats[st][k][0], a.mean + tile * R + k);
-                cp_async4(&stats[st][k][1], a.rstd + tile * R + k);
-            }
-        }
-        cp_async_commit();
-    };
-    long long tile = blockIdx.x;
-    if (threadIdx.x == 0) {
-        for (int st = 0; st < kNormStages; ++st)
+    if (tid == 0) {
+        for (int st = 0; st < ring.stages; ++st)
             mbar_init(&full[st], 1);
         fence_mbarrier_init();
+        for (int st = 0; st < ring.stages; ++st)
+            if (blockIdx.x + static_cast<long long>(st) * gridDim.x < steps)
+                fetch(st, blockIdx.x + static_cast<long long>(st) * gridDim.x);
     }
-    __syncthreads();
-#pragma unroll
-    for (int st = 0; st < kNormStages; ++st)
-        fetch(st, tile + static_cast<long long>(st) * gridDim.x);
-    for (int c = threadIdx.x; c < W; c += T)
-        w[c] = a.w ? a.w[c] : 1.0f;
     f2_t wv[NQ][2], dw[NQ][2], db[NQ][2];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         quad_params<V>(a.w, 1.0f, col(j), T, W, wv[j]);
         dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = f2_both(0.0f);
     }
+    // a step's statistics are fetched one step ahead
+    float mean[R], rstd[R];
+    auto statistics = [&](long long step) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const long long row = step * R + k;
+            mean[k] = row < a.rows ? a.mean[row] : 0.0f;
+            rstd[k] = row < a.rows ? a.rstd[row] : 0.0f;
+        }
+    };
+    if (blockIdx.x < steps)
+        statistics(blockIdx.x);
+    __syncthreads();
 
-    int st = 0;
-    uint32_t phase = 0;
-    for (; tile < tiles; tile += gridDim.x) {
-        const int here = rows_of(tile);
-        cp_async_wait<kNormStages - 1>();
-        const bool ok = mbar_wait_bounded(&full[st], phase, kBulkPolls);
-        if (__syncthreads_or(!ok)) {
-            if (threadIdx.x == 0) {
-                raise_device_error(kErrTrainCopy);
-                // the copies still in flight are waited for, with the same bound
-                if (tile + gridDim.x < tiles)
-                    mbar_wait_bounded(&full[st ^ 1], st ? phase ^ 1u : phase, kBulkPolls);
+    int turn = 0;
+    for (long long step = blockIdx.x; step < steps; step += gridDim.x, turn ^= 1) {
+        const long long row = step * R;
+        const int here = a.rows - row < R ? static_cast<int>(a.rows - row) : R;
+        float q[R];
+        f2_t h[R][NQ][2], g[R][NQ][2];
+        float sums[2 * R];
+        const bool ok = ring.wait();
+        const X *xs = reinterpret_cast<const X *>(ring.at() + in16(x, row * W));
+        const Y *gs = reinterpret_cast<const Y *>(ring.at() + args.s.x_bytes + in16(dy, row * W));
+        const float *es = reinterpret_cast<const float *>(ring.at() + args.s.x_bytes + args.s.y_bytes +
+                                                          in16(a.ds, row * W));
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int n = k < here ? W : 0;
+            const f2_t m = f2_both(-mean[k]), q2 = f2_both(rstd[k]);
+            q[k] = rstd[k];
+            f2_t s0 = f2_both(0.0f), s1 = s0;
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                QX xq;
+                QY gq;
+                xq.template load<false>(xs + k * W, col(j), T, n);
+                gq.template load<false>(gs + k * W, col(j), T, n);
+                xq.pairs(h[k][j]);
+                gq.pairs(g[k][j]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // what is behind the row, or a row that is not there, has g = 0 and adds nothing
+                    h[k][j][i] = f2_mul(f2_add(h[k][j][i], m), q2);
+                    dw[j][i] = f2_fma(g[k][j][i], h[k][j][i], dw[j][i]);
+                    db[j][i] = f2_add(db[j][i], g[k][j][i]);
+                    g[k][j][i] = f2_mul(g[k][j][i], wv[j][i]);
+                    s0 = f2_add(s0, g[k][j][i]);
+                    s1 = f2_fma(g[k][j][i], h[k][j][i], s1);
+                }
+            }
+            float lo, hi;
+            f2_unpack(s0, lo, hi);
+            sums[2 * k] = lo + hi;
+            f2_unpack(s1, lo, hi);
+            sums[2 * k + 1] = lo + hi;
+        }
+        if (step + gridDim.x < steps)
+            statistics(step + gridDim.x);
+        // slots by turns: those of this step are written again two steps on, after the next
+        // step's barrier, which every reader of them has passed
+        if (block_sums<2 * R, WARPS>(sums, slots[turn], !ok)) {
+            if (tid == 0) {
+                const long long more = (steps - 1 - step) / gridDim.x;
+                const int started = ring.stages - (step == blockIdx.x ? 1 : 2);
+                ring.drain(more < started ? static_cast<int>(more) : started);
             }
             return;
         }
-        const X *xs = reinterpret_cast<const X *>(buf + st * stage + in16(x, tile * R * W));
-        const Y *gs = reinterpret_cast<const Y *>(buf + st * stage + args.x_bytes + in16(dy, tile * R * W));
-        const float *es = reinterpret_cast<const float *>(buf + st * stage + args.x_bytes + args.dy_bytes +
-                                                          in16(a.ds, tile * R * W));
-        if (warp / share < here) {
-            const int k = warp / share, part = warp - k * share;
-            const X *xk = xs + k * W;
-            const Y *gk = gs + k * W;
-            const f2_t m = f2_both(-stats[st][k][0]), q = f2_both(stats[st][k][1]);
-            f2_t s0 = f2_both(0.0f), s1 = s0;
-            auto one = [&](auto all, int c) {
-                constexpr bool ALL = decltype(all)::value;
-                QX xq;
-                QY gq;
-                QF wq;
-                f2_t h[2], g[2], wc[2];
-                xq.template load<ALL>(xk, c, 32, W);
-                gq.template load<ALL>(gk, c, 32, W);
-                wq.template load<ALL>(w, c, 32, W);
-                xq.pairs(h);
-                gq.pairs(g);
-                wq.pairs(wc);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    g[i] = f2_mul(g[i], wc[i]);
-                    s0 = f2_add(s0, g[i]);
-                    s1 = f2_fma(g[i], f2_mul(f2_add(h[i], m), q), s1);
-                }
-            };
-            int c = part * 128;
-#pragma unroll 4
-            for (; c + 128 <= W; c += share * 128)
-                one(std::true_type{}, c + lane * V);
-            if (c < W)
-                one(std::false_type{}, c + lane * V);
-            float m0, m1, hi;
-            f2_unpack(s0, m0, hi);
-            m0 += hi;
-            f2_unpack(s1, m1, hi);
-            m1 += hi;
-            warp_sum2(m0, m1);
-            if (lane == 0)
-                parts[k][part] = make_float2(m0, m1);
+        // every thread is past the step before this one, ds too: its stage is free
+        if (tid == 0 && step != blockIdx.x) {
+            const long long ahead = step + static_cast<long long>(ring.stages - 1) * gridDim.x;
+            if (ahead < steps)
+                fetch(ring.st ? ring.st - 1 : ring.stages - 1, ahead);
         }
-        __syncthreads();
-        float *dxp = a.dx + tile * R * W;
-        for (int k = 0; k < here; ++k, dxp += W, xs += W, gs += W, es += W) {
-            const float rstd = stats[st][k][1];
-            const f2_t m = f2_both(-stats[st][k][0]), q = f2_both(rstd);
-            float m0 = parts[k][0].x, m1 = parts[k][0].y;
-            for (int p = 1; p < share; ++p) {
-                m0 += parts[k][p].x;
-                m1 += parts[k][p].y;
+        ring.next();
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (k < here) {
+                // q (g - m0 - h m1) as q (g - h m1) - q m0
+                const f2_t q2 = f2_both(q[k]), c1 = f2_both(-sums[2 * k + 1] * a.inv_w),
+                           c0 = f2_both(-q[k] * (sums[2 * k] * a.inv_w));
+                float *dxp = a.dx + (row + k) * W;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    f2_t o[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        o[i] = f2_fma(f2_fma(h[k][j][i], c1, g[k][j][i]), q2, c0);
+                    if (a.ds) {
+                        QF eq;
+                        f2_t t[2];
+                        eq.template load<false>(es + k * W, col(j), T, W);
+                        eq.pairs(t);
+                        o[0] = f2_add(o[0], t[0]);
+                        o[1] = f2_add(o[1], t[1]);
+                    }
+                    QF::template store<false>(dxp, col(j), T, W, o);
+                }
             }
-            const f2_t c1 = f2_both(-m1 * a.inv_w), c0 = f2_both(-rstd * (m0 * a.inv_w));
-            auto one = [&](auto all, int j) {
-                constexpr bool ALL = decltype(all)::value;
-                QX xq;
-                QY gq;
-                f2_t h[2], g[2], o[2];
-                xq.template load<ALL>(xs, col(j), T, W);
-                gq.template load<ALL>(gs, col(j), T, W);
-                xq.pairs(h);
-                gq.pairs(g);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    h[i] = f2_mul(f2_add(h[i], m), q);
-                    dw[j][i] = f2_fma(g[i], h[i], dw[j][i]);
-                    db[j][i] = f2_add(db[j][i], g[i]);
-                    o[i] = f2_fma(f2_fma(h[i], c1, f2_mul(g[i], wv[j][i])), q, c0);
-                }
-                if (a.ds) {
-                    QF eq;
-                    f2_t t[2];
-                    eq.template load<ALL>(es, col(j), T, W);
-                    eq.pairs(t);
-                    o[0] = f2_add(o[0], t[0]);
-                    o[1] = f2_add(o[1], t[1]);
-                }
-                QF::template store<ALL>(dxp, col(j), T, W, o);
-            };
-#pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                if (4 * T * (j + 1) <= W)
-                    one(std::true_type{}, j);
-                else if (4 * T * j < W)
-                    one(std::false_type{}, j);
-            }
-        }
-        __syncthreads();  // every thread is done with the stage
-        fetch(st, tile + static_cast<long long>(kNormStages) * gridDim.x);
-        if (++st == kNormStages) {
-            st = 0;
-            phase ^= 1u;
-        }
     }
     if (!a.part)
         return;

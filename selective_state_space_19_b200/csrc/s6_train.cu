@@ -81,79 +81,55 @@ int check_norm_dims(const s6_norm_dims *dims) {
     return S6_OK;
 }
 
-// Blocks that fit an SM beside one another with `smem` bytes each (227 KB in all,
-// 1 KB of it the system's for each block).
-constexpr int kSmemSM = 227 * 1024, kSmemBlock = 1024;
-int64_t blocks_of_smem(int64_t smem) { return std::max<int64_t>(1, kSmemSM / (smem + kSmemBlock)); }
-
-struct NormPlan {
-    int elems;  // elements of a row that a thread holds, at most
-    int threads;
-    int tile;   // rows that a block takes at a time (backward through shared memory)
-    int64_t blocks, smem;
+// Rows of one warp: as many blocks as are resident, which walk the rows.
+struct NormWarpPlan {
+    int elems;  // elements of a row that a lane holds, at most
+    int64_t blocks;
 };
 
-// Rows of one warp: as many blocks as are resident, which walk the rows.
-NormPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd) {
-    NormPlan p;
+NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd) {
+    NormWarpPlan p;
     p.elems = static_cast<int>(4 * ceil_div(width, 128));
-    p.threads = 32 * s6::kNormBlockWarps;
-    p.tile = p.smem = 0;
     p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps),
                         kSMs * s6::norm_warps_resident(p.elems, bwd) / s6::kNormBlockWarps);
     return p;
 }
 
-// Blocks of the backward through shared memory on an SM, at 128 registers a thread.
-constexpr int norm_tile_resident(int64_t warps) { return static_cast<int>(16 / warps); }
-
-int64_t norm_params_bytes(int64_t width) { return (width + 3) / 4 * 4 * static_cast<int64_t>(sizeof(float)); }
-
-// Forward through shared memory: 8 warps where two blocks of them fit an SM, or
-// else as many as one block can have.
-NormPlan norm_rows_plan(int64_t rows, int64_t width, int64_t row_bytes) {
-    NormPlan p;
-    p.elems = p.tile = 0;
-    const int64_t fixed = 2 * norm_params_bytes(width), warp = s6::kNormStages * row_bytes;
-    int64_t warps = s6::kNormRowWarps;
-    while (warps > 1 && fixed + warps * warp > kSmemSM - kSmemBlock)
-        warps /= 2;
-    p.threads = static_cast<int>(32 * warps);
-    p.smem = fixed + warps * warp;
-    p.blocks = std::min(ceil_div(rows, warps), kSMs * std::min<int64_t>(blocks_of_smem(p.smem), 2));
-    return p;
-}
-
-// Backward through shared memory: 4, 8 or 16 warps with as many quads of columns a
-// thread as hold the row (up to 5, 5 and 4); then the most rows of a tile that
-// leave room for the blocks that the registers allow on an SM.
-template <typename Bytes>
-NormPlan norm_tile_plan(int64_t rows, int64_t width, Bytes tile_bytes) {
-    NormPlan p;
-    const int64_t quads = ceil_div(width, 128);  // of a warp
-    const int64_t warps = quads <= 20 ? 4 : quads <= 40 ? 8 : 16;
-    p.elems = static_cast<int>(4 * ceil_div(quads, warps));
-    const int64_t fixed = norm_params_bytes(width), most = norm_tile_resident(warps);
-    const int64_t statics = 2 * kSmemBlock;  // the kernel's own shared arrays and the system's part
-    int64_t tile = std::min<int64_t>(s6::kNormTileRows, warps);
-    while (tile > 1 && fixed + s6::kNormStages * tile_bytes(tile) > kSmemSM / most - statics)
-        tile /= 2;
-    p.tile = static_cast<int>(tile);
-    p.threads = static_cast<int>(32 * warps);
-    p.smem = fixed + s6::kNormStages * tile_bytes(tile);
-    p.blocks = std::min(ceil_div(rows, tile), kSMs * std::min(blocks_of_smem(p.smem + kSmemBlock), most));
-    return p;
-}
-
-// A tile's buffers: x, dy and, where it is given, ds.
-struct NormTileBytes {
-    int64_t width, sx, sy;
-    bool ds;
-    int64_t x(int64_t tile) const { return s6::row_buffer_bytes(tile * width * sx); }
-    int64_t dy(int64_t tile) const { return s6::row_buffer_bytes(tile * width * sy); }
-    int64_t e(int64_t tile) const { return ds ? s6::row_buffer_bytes(tile * width * 4) : 0; }
-    int64_t operator()(int64_t tile) const { return x(tile) + dy(tile) + e(tile); }
+// Rows of a block: threads, quads of columns of a thread, rows of a step, blocks on
+// an SM.
+struct NormBlockPlan {
+    int threads, quads, rows, per_sm;
+    int64_t blocks;
 };
+
+constexpr int kSmemSM = 227 * 1024, kSmemBlock = 2 * 1024;  // of an SM; a block's other shared memory, at most
+constexpr int norm_block_per_sm(int threads, bool bwd) {    // by the registers (the kernels' launch bounds)
+    return bwd ? 512 / threads : threads == 512 ? 1 : 768 / threads;
+}
+
+// Two rows a step where two steps of them fit in shared memory beside at least
+// three quarters of the blocks that the registers allow, else one.  `row_bytes`:
+// what a row takes of all tensors.
+NormBlockPlan norm_block_plan(int64_t rows, int64_t width, int64_t row_bytes, bool bwd) {
+    NormBlockPlan p;
+    p.threads = width <= 12 * 128 ? 128 : width <= 12 * 256 ? 256 : 512;
+    p.quads = static_cast<int>(std::max<int64_t>(2, ceil_div(width, 4 * p.threads)));
+    const int most = norm_block_per_sm(p.threads, bwd);
+    auto fits = [&](int64_t r) {  // blocks with two stages of r rows (16 bytes a tensor beside them)
+        return static_cast<int>(kSmemSM / (2 * (r * row_bytes + 96) + kSmemBlock));
+    };
+    p.rows = p.quads <= 3 && 4 * std::min(most, fits(2)) >= 3 * most ? 2 : 1;
+    p.per_sm = std::min(most, std::max(1, fits(p.rows)));
+    p.blocks = std::min(ceil_div(rows, p.rows), kSMs * p.per_sm);
+    return p;
+}
+
+// As many stages as fit, 2 to kNormMaxStages; returns the shared memory.
+int norm_stages(s6::NormStream &s, const NormBlockPlan &p) {
+    const int fit = (kSmemSM / p.per_sm - kSmemBlock) / s.stage();
+    s.stages = std::max(2, std::min(fit, s6::kNormMaxStages));
+    return s.stages * s.stage();
+}
 
 // Runs of rows of the wide backward's second kernel: enough blocks to fill the
 // SMs at its 128-thread blocks, whatever the vector width.
@@ -163,38 +139,69 @@ int64_t norm_wide_runs(int64_t rows, int64_t width) {
 }
 
 template <typename X, typename Y, int V, int NQ>
-void norm_launch(const s6::NormFwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    s6::s6_layernorm_fwd_kernel<X, Y, V, NQ><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
+void norm_launch(const s6::NormFwdArgs &a, unsigned grid, cudaStream_t st) {
+    s6::s6_layernorm_fwd_kernel<X, Y, V, NQ><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
 }
 
 template <typename X, typename Y, int V, int NQ>
-void norm_launch(const s6::NormBwdArgs &a, const NormPlan &p, cudaStream_t st) {
-    s6::s6_layernorm_bwd_kernel<X, Y, V, NQ><<<static_cast<unsigned>(p.blocks), p.threads, 0, st>>>(a);
+void norm_launch(const s6::NormBwdArgs &a, unsigned grid, cudaStream_t st) {
+    s6::s6_layernorm_bwd_kernel<X, Y, V, NQ><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
 }
 
 // Rows of one warp: the instantiation that holds p.elems elements a lane.
 template <typename X, typename Y, int V, typename Args>
-int norm_warp_rows(const Args &a, const NormPlan &p, cudaStream_t st) {
+int norm_warp_rows(const Args &a, const NormWarpPlan &p, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>(p.blocks);
     if (p.elems <= 4)
-        norm_launch<X, Y, V, 1>(a, p, st);
+        norm_launch<X, Y, V, 1>(a, grid, st);
     else if (p.elems <= 8)
-        norm_launch<X, Y, V, 2>(a, p, st);
+        norm_launch<X, Y, V, 2>(a, grid, st);
     else if (p.elems <= 12)
-        norm_launch<X, Y, V, 3>(a, p, st);
+        norm_launch<X, Y, V, 3>(a, grid, st);
     else
-        norm_launch<X, Y, V, 4>(a, p, st);
+        norm_launch<X, Y, V, 4>(a, grid, st);
     return launch_status(cudaGetLastError());
 }
 
-// Launches a kernel with more dynamic shared memory than the default 48 KB (the
-// attribute is the device's own, and setting it costs little).
-template <typename Args>
-int launch_smem(void (*kern)(Args), const NormPlan &p, cudaStream_t st, const Args &a) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(p.smem)) !=
-        cudaSuccess)
+template <typename X, typename Y, int V, int NQ, int R, int T>
+auto norm_block_kernel(const s6::NormFwdBlockArgs &) {
+    return s6::s6_layernorm_fwd_block_kernel<X, Y, V, NQ, R, T, norm_block_per_sm(T, false)>;
+}
+template <typename X, typename Y, int V, int NQ, int R, int T>
+auto norm_block_kernel(const s6::NormBwdBlockArgs &) {
+    return s6::s6_layernorm_bwd_block_kernel<X, Y, V, NQ, R, T, norm_block_per_sm(T, true)>;
+}
+
+// Launches with more dynamic shared memory than the default 48 KB (the attribute
+// is the device's own; setting it costs little).
+template <typename X, typename Y, int V, int NQ, int R, int T, typename Args>
+int norm_block_launch(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
+    auto kern = norm_block_kernel<X, Y, V, NQ, R, T>(a);
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return S6_ERR_CUDA;
-    kern<<<static_cast<unsigned>(p.blocks), p.threads, static_cast<size_t>(p.smem), st>>>(a);
+    kern<<<static_cast<unsigned>(p.blocks), T, static_cast<size_t>(smem), st>>>(a);
     return launch_status(cudaGetLastError());
+}
+
+template <typename X, typename Y, int V, int NQ, int T, typename Args>
+int norm_block_r(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
+    return p.rows == 1 ? norm_block_launch<X, Y, V, NQ, 1, T>(a, p, smem, st)
+                       : norm_block_launch<X, Y, V, NQ, 2, T>(a, p, smem, st);
+}
+
+// 2 or 3 quads of 128, 256 or 512 threads, and 4 of 512 (norm_block_plan).
+template <typename X, typename Y, int V, typename Args>
+int norm_block_rows(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
+    if (p.threads == 128)
+        return p.quads == 2 ? norm_block_r<X, Y, V, 2, 128>(a, p, smem, st)
+                            : norm_block_r<X, Y, V, 3, 128>(a, p, smem, st);
+    if (p.threads == 256)
+        return p.quads == 2 ? norm_block_r<X, Y, V, 2, 256>(a, p, smem, st)
+                            : norm_block_r<X, Y, V, 3, 256>(a, p, smem, st);
+    return p.quads == 2   ? norm_block_r<X, Y, V, 2, 512>(a, p, smem, st)
+           : p.quads == 3 ? norm_block_r<X, Y, V, 3, 512>(a, p, smem, st)
+                          : norm_block_launch<X, Y, V, 4, 1, 512>(a, p, smem, st);
 }
 
 template <typename X, typename Y, int V>
@@ -207,33 +214,16 @@ int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
     }
     if (a.width <= s6::kNormWarpWidth)
         return norm_warp_rows<X, Y, V>(a, norm_warp_plan(a.rows, a.width, false), st);
-    s6::NormRowsArgs r;
+    const int64_t sx = sizeof(X), sr = a.r ? sizeof(Y) : 0;
+    const NormBlockPlan p = norm_block_plan(a.rows, a.width, a.width * (sx + sr), false);
+    const int64_t n = p.rows * static_cast<int64_t>(a.width);
+    s6::NormFwdBlockArgs r;
     r.n = a;
-    r.x_bytes = s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(X)));
-    r.r_bytes = a.r ? s6::row_buffer_bytes(a.width * static_cast<int64_t>(sizeof(Y))) : 0;
-    return launch_smem(s6::s6_layernorm_fwd_rows_kernel<X, Y, V>,
-                       norm_rows_plan(a.rows, a.width, r.x_bytes + r.r_bytes), st, r);
-}
-
-// Quads of a thread and threads of a block: 2 to 5 with 4 warps, 3 to 5 with 8, 3 or 4
-// with 16.
-template <typename X, typename Y, int V, int NQ, int T>
-int norm_tile_t(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
-    return launch_smem(s6::s6_layernorm_bwd_tile_kernel<X, Y, V, NQ, T, norm_tile_resident(T / 32)>, p, st, a);
-}
-template <typename X, typename Y, int V>
-int norm_tile(const s6::NormTileArgs &a, const NormPlan &p, cudaStream_t st) {
-    const int nq = p.elems / 4;
-    if (p.threads == 128)
-        return nq <= 2   ? norm_tile_t<X, Y, V, 2, 128>(a, p, st)
-               : nq == 3 ? norm_tile_t<X, Y, V, 3, 128>(a, p, st)
-               : nq == 4 ? norm_tile_t<X, Y, V, 4, 128>(a, p, st)
-                         : norm_tile_t<X, Y, V, 5, 128>(a, p, st);
-    if (p.threads == 256)
-        return nq <= 3   ? norm_tile_t<X, Y, V, 3, 256>(a, p, st)
-               : nq == 4 ? norm_tile_t<X, Y, V, 4, 256>(a, p, st)
-                         : norm_tile_t<X, Y, V, 5, 256>(a, p, st);
-    return nq <= 3 ? norm_tile_t<X, Y, V, 3, 512>(a, p, st) : norm_tile_t<X, Y, V, 4, 512>(a, p, st);
+    r.s.x_bytes = s6::row_buffer_bytes(n * sx);
+    r.s.y_bytes = a.r ? s6::row_buffer_bytes(n * sr) : 0;
+    r.s.e_bytes = 0;
+    const int smem = norm_stages(r.s, p);
+    return norm_block_rows<X, Y, V>(r, p, smem, st);
 }
 
 template <typename X, typename Y, int V>
@@ -257,20 +247,20 @@ int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db,
         a.part = params ? part : nullptr;
         int rc;
         if (a.width <= s6::kNormWarpWidth) {
-            const NormPlan p = norm_warp_plan(a.rows, a.width, true);
+            const NormWarpPlan p = norm_warp_plan(a.rows, a.width, true);
             parts = p.blocks;
             rc = norm_warp_rows<X, Y, V>(a, p, st);
         } else {
-            s6::NormTileArgs t;
+            const int64_t sx = sizeof(X), sy = sizeof(Y), se = a.ds ? sizeof(float) : 0;
+            const NormBlockPlan p = norm_block_plan(a.rows, a.width, a.width * (sx + sy + se), true);
+            const int64_t n = p.rows * static_cast<int64_t>(a.width);
+            s6::NormBwdBlockArgs t;
             t.n = a;
-            const NormTileBytes bytes{a.width, sizeof(X), sizeof(Y), a.ds != nullptr};
-            const NormPlan p = norm_tile_plan(a.rows, a.width, bytes);
+            t.s.x_bytes = s6::row_buffer_bytes(n * sx);
+            t.s.y_bytes = s6::row_buffer_bytes(n * sy);
+            t.s.e_bytes = a.ds ? s6::row_buffer_bytes(n * se) : 0;
             parts = p.blocks;
-            t.tile = p.tile;
-            t.x_bytes = static_cast<int>(bytes.x(p.tile));
-            t.dy_bytes = static_cast<int>(bytes.dy(p.tile));
-            t.ds_bytes = static_cast<int>(bytes.e(p.tile));
-            rc = norm_tile<X, Y, V>(t, p, st);
+            rc = norm_block_rows<X, Y, V>(t, p, norm_stages(t.s, p), st);
         }
         if (rc != S6_OK)
             return rc;
@@ -561,13 +551,10 @@ int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims) {
         return dims->rows * static_cast<int64_t>(sizeof(float2)) + norm_wide_runs(dims->rows, dims->width) * row;
     if (dims->width <= s6::kNormWarpWidth)
         return norm_warp_plan(dims->rows, dims->width, true).blocks * row;
-    // with or without ds: the smaller rows may give more blocks, or the larger ones (shorter tiles)
-    NormTileBytes bytes{dims->width, static_cast<int64_t>(io_size(dims->x_dtype)),
-                        static_cast<int64_t>(io_size(dims->y_dtype)), false};
-    int64_t blocks = norm_tile_plan(dims->rows, dims->width, bytes).blocks;
-    bytes.ds = true;
-    blocks = std::max(blocks, norm_tile_plan(dims->rows, dims->width, bytes).blocks);
-    return blocks * row;
+    // with and without ds
+    const int64_t io = dims->width * static_cast<int64_t>(io_size(dims->x_dtype) + io_size(dims->y_dtype));
+    return row * std::max(norm_block_plan(dims->rows, dims->width, io, true).blocks,
+                          norm_block_plan(dims->rows, dims->width, io + 4 * dims->width, true).blocks);
 }
 
 int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean, const float *rstd, const float *w,

@@ -135,15 +135,6 @@ __device__ __forceinline__ float f2_sum(f2_t a, f2_t b) {
 }
 
 // ------------------------------------------------- rows into shared memory
-__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Shared bytes that rows of n bytes in all may take: they keep their place within 16 bytes.
 __host__ __device__ constexpr int row_buffer_bytes(long long n) { return static_cast<int>((n + 15) / 16 * 16 + 16); }
 
@@ -155,44 +146,40 @@ __device__ __forceinline__ int in16(const T *p, long long at) {
                              static_cast<uint32_t>(at) * static_cast<uint32_t>(sizeof(T))) & 15u);
 }
 
-// A stretch of a tensor to be copied into shared memory by one bulk copy, which
-// must begin and end on 16-byte boundaries of global memory: the stretch keeps
-// its place within 16 bytes, and the up to 15 bytes around it that the copy
-// brings along are its neighbours in the tensor.  Where the tensor itself begins
-// or ends off a boundary, the copy stays inside it and the few elements between
-// are moved singly.
-struct BulkSpan {
-    const unsigned char *from;
-    uint32_t at, bytes;  // place of the copy in the buffer, and its size (0: none)
-};
-
-// Elements [first, first + n) of the `total` at `tensor` into buf (element
-// `first` lands at buf + in16 of its address); moves the single elements.
-template <typename T>
-__device__ __forceinline__ BulkSpan bulk_span(unsigned char *buf, const T *tensor, long long total, long long first,
-                                              long long n) {
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(tensor), end = begin + total * sizeof(T);
-    const uintptr_t a = begin + first * sizeof(T), b = a + n * sizeof(T), base = a & ~static_cast<uintptr_t>(15);
-    uintptr_t lo = base, hi = (b + 15) & ~static_cast<uintptr_t>(15);
-    if (lo < begin)
-        lo += 16;
-    if (hi > end)
-        hi -= 16;
-    if (hi <= lo)
-        lo = hi = b;  // all of it singly
-    for (uintptr_t p = a; p < lo; p += sizeof(T))
-        *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
-    for (uintptr_t p = hi > a ? hi : a; p < b; p += sizeof(T))
-        *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
-    BulkSpan s;
-    s.from = reinterpret_cast<const unsigned char *>(lo);
-    s.at = static_cast<uint32_t>(lo - base);
-    s.bytes = static_cast<uint32_t>(hi - lo);
-    return s;
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
 }
-__device__ __forceinline__ void bulk_start(unsigned char *buf, const BulkSpan &s, uint64_t *bar) {
-    if (s.bytes)
-        bulk_load(buf + s.at, s.from, s.bytes, bar);
+
+// Starts the bulk copy of the stretch [a, a + n) of a tensor's memory [begin, end)
+// into buf and adds its bytes to what `bar` expects (the caller arrives).  A bulk copy begins
+// and ends on 16-byte boundaries of global memory: the stretch keeps its place
+// within 16 bytes (a lands at buf + a % 16), and the up to 15 bytes around it
+// that come along are its neighbours in the tensor.  Where the tensor itself
+// begins or ends off a boundary, the copy stays inside it and the few elements
+// between are moved singly, by this thread.
+template <typename T>
+__device__ __forceinline__ void bulk_fetch(unsigned char *buf, uintptr_t a, uint32_t n, uintptr_t begin,
+                                           uintptr_t end, uint64_t *bar) {
+    const uintptr_t base = a & ~static_cast<uintptr_t>(15), b = a + n;
+    uintptr_t lo = base, hi = (b + 15) & ~static_cast<uintptr_t>(15);
+    if (lo < begin || hi > end) {
+        if (lo < begin)
+            lo += 16;
+        if (hi > end)
+            hi -= 16;
+        if (hi <= lo)
+            lo = hi = b;  // all of it singly
+        for (uintptr_t p = a; p < lo; p += sizeof(T))
+            *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
+        for (uintptr_t p = hi > a ? hi : a; p < b; p += sizeof(T))
+            *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
+        if (hi == lo)
+            return;
+    }
+    const uint32_t bytes = static_cast<uint32_t>(hi - lo);
+    mbar_expect_tx(bar, bytes);
+    bulk_load(buf + (lo - base), reinterpret_cast<const void *>(lo), bytes, bar);
 }
 
 constexpr uint32_t kBulkPolls = 1u << 22;  // bound of a wait for a copy, far above any that arrives
@@ -215,6 +202,54 @@ __device__ __forceinline__ void warp_sum2(float &a, float &b) {
         v += __shfl_xor_sync(0xffffffffu, v, o);
     a = __shfl_sync(0xffffffffu, v, 0);
     b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// N sums (1, 2 or 4) over a block of WARPS warps (4, 8 or 16), in every thread
+// and in a fixed order.  The walk over a warp halves the number of sums a lane
+// carries with each of its first steps; the second walk, over the warps' slots,
+// is made by every warp.  `any`: ORed over the block.  One barrier; `slots` must
+// not be in use by readers of an earlier call (see the callers).
+template <int N, int WARPS>
+__device__ __forceinline__ bool block_sums(float (&v)[N], float (&slots)[4][16], bool any) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float t;
+    if constexpr (N == 4) {
+        const bool low = (lane & 16) == 0, lo8 = (lane & 8) == 0;
+        float a = low ? v[0] : v[2], b = low ? v[1] : v[3];
+        a += __shfl_xor_sync(0xffffffffu, low ? v[2] : v[0], 16);
+        b += __shfl_xor_sync(0xffffffffu, low ? v[3] : v[1], 16);
+        t = lo8 ? a : b;
+        t += __shfl_xor_sync(0xffffffffu, lo8 ? b : a, 8);
+    } else if constexpr (N == 2) {
+        const bool low = (lane & 16) == 0;
+        t = low ? v[0] : v[1];
+        t += __shfl_xor_sync(0xffffffffu, low ? v[1] : v[0], 16);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+    } else {
+        t = v[0];
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    constexpr int span = 32 / N;  // lanes that carry one sum
+    if (lane % span == 0)
+        slots[lane / span][warp] = t;
+    const bool bad = __syncthreads_or(any);
+    // lane l of every warp takes slots l % span, l % span + span, ... of sum l / span
+    t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WARPS; k += span)
+        if (k + lane % span < WARPS)
+            t += slots[lane / span][k + lane % span];
+#pragma unroll
+    for (int o = (span < WARPS ? span : WARPS) / 2; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k] = __shfl_sync(0xffffffffu, t, k * span);
+    return bad;
 }
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
