@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
     using QX = Quad<X, V>;
     using QY = Quad<Y, V>;
     const int lane = threadIdx.x & 31, W = a.width;
-    auto col = [&](int j) { return lane * V + 128 * j; };  // of quad j
+    auto col = [&](int j) { return lane * V + 128 * j; };  // of quad j; only the last can pass the row's end
     f2_t wv[NQ][2], bv[NQ][2];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
     auto fetch = [&](long long at) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            xr[j].template load<false>(x + at * W, col(j), 32, W);
+            xr[j].load(x + at * W, j + 1 < NQ, col(j), 32, W);
             if (r)
-                rr[j].template load<false>(r + at * W, col(j), 32, W);
+                rr[j].load(r + at * W, j + 1 < NQ, col(j), 32, W);
         }
     };
     if (row < a.rows)
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
                 v[j][0] = f2_add(v[j][0], t[0]);
                 v[j][1] = f2_add(v[j][1], t[1]);
                 if (s)
-                    QX::template store<false>(s + row * W, col(j), 32, W, v[j]);
+                    QX::store(s + row * W, j + 1 < NQ, col(j), 32, W, v[j]);
             }
             t0 = f2_add(t0, v[j][0]);
             t1 = f2_add(t1, v[j][1]);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             f2_t m[2];
-            quad_where<V>(-mean, col(j), 32, W, m);
+            quad_where<V>(-mean, j + 1 < NQ, col(j), 32, W, m);
             v[j][0] = f2_add(v[j][0], m[0]);
             v[j][1] = f2_add(v[j][1], m[1]);
             t0 = f2_fma(v[j][0], v[j][0], t0);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         for (int j = 0; j < NQ; ++j) {
             const f2_t o[2] = {f2_fma(f2_mul(v[j][0], q), wv[j][0], bv[j][0]),
                                f2_fma(f2_mul(v[j][1], q), wv[j][1], bv[j][1])};
-            QY::template store<false>(y + row * W, col(j), 32, W, o);
+            QY::store(y + row * W, j + 1 < NQ, col(j), 32, W, o);
         }
     }
 }
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         rstd = a.rstd[at];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            xr[j].template load<false>(x + at * W, col(j), 32, W);
-            gr[j].template load<false>(dy + at * W, col(j), 32, W);
+            xr[j].load(x + at * W, j + 1 < NQ, col(j), 32, W);
+            gr[j].load(dy + at * W, j + 1 < NQ, col(j), 32, W);
         }
     };
     if (row < a.rows)
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         if (a.ds) {
 #pragma unroll
             for (int j = 0; j < NQ; ++j)
-                ds[j].template load<false>(a.ds + row * W, col(j), 32, W);
+                ds[j].load(a.ds + row * W, j + 1 < NQ, col(j), 32, W);
         }
         float m0, m1, hi;
         f2_unpack(s0, m0, hi);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
                 o[0] = f2_add(o[0], t[0]);
                 o[1] = f2_add(o[1], t[1]);
             }
-            QF::template store<false>(a.dx + row * W, col(j), 32, W, o);
+            QF::store(a.dx + row * W, j + 1 < NQ, col(j), 32, W, o);
         }
     }
 
@@ -332,17 +332,17 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
                 f2_t t[2];
                 Quad<float, V> at;
                 if (k) {
-                    at.template load<true>(sums[0], col(j), 32, 0);
+                    at.load(sums[0], true, col(j), 32, 0);
                     at.pairs(t);
                     dw[j][0] = f2_add(t[0], dw[j][0]);
                     dw[j][1] = f2_add(t[1], dw[j][1]);
-                    at.template load<true>(sums[1], col(j), 32, 0);
+                    at.load(sums[1], true, col(j), 32, 0);
                     at.pairs(t);
                     db[j][0] = f2_add(t[0], db[j][0]);
                     db[j][1] = f2_add(t[1], db[j][1]);
                 }
-                QF::template store<true>(sums[0], col(j), 32, 0, dw[j]);
-                QF::template store<true>(sums[1], col(j), 32, 0, db[j]);
+                QF::store(sums[0], true, col(j), 32, 0, dw[j]);
+                QF::store(sums[1], true, col(j), 32, 0, db[j]);
             }
         }
         __syncthreads();
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
     const int tid = threadIdx.x, W = a.width;
     const X *x = static_cast<const X *>(a.x);
     const Y *r = static_cast<const Y *>(a.r);
-    auto col = [&](int j) { return tid * V + 4 * T * j; };
+    auto col = [&](int j) { return tid * V + 4 * T * j; };  // only the last quad can pass the row's end
     const long long steps = (a.rows + R - 1) / R, total = a.rows * W;
     NormRing ring{s6_norm_smem, full, args.s.stages, args.s.x_bytes + args.s.y_bytes, 0, 0u};
 
@@ -459,22 +459,24 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
         // a row that is not there is read as zeros
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int n = k < here ? W : 0;
             f2_t t0 = f2_both(0.0f), t1 = t0;
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
+                v[k][j][0] = v[k][j][1] = f2_both(0.0f);
+                if (k > 0 && k >= here)
+                    continue;
                 QX q;
-                q.template load<false>(xs + k * W, col(j), T, n);
+                q.load(xs + k * W, j + 1 < NQ, col(j), T, W);
                 q.pairs(v[k][j]);
                 if (r) {
                     QY p;
                     f2_t t[2];
-                    p.template load<false>(rs + k * W, col(j), T, n);
+                    p.load(rs + k * W, j + 1 < NQ, col(j), T, W);
                     p.pairs(t);
                     v[k][j][0] = f2_add(v[k][j][0], t[0]);
                     v[k][j][1] = f2_add(v[k][j][1], t[1]);
                     if (a.s)
-                        QX::template store<false>(static_cast<X *>(a.s) + (row + k) * W, col(j), T, n, v[k][j]);
+                        QX::store(static_cast<X *>(a.s) + (row + k) * W, j + 1 < NQ, col(j), T, W, v[k][j]);
                 }
                 t0 = f2_add(t0, v[k][j][0]);
                 t1 = f2_add(t1, v[k][j][1]);
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
                 f2_t m[2];
-                quad_where<V>(-mean[k], col(j), T, W, m);
+                quad_where<V>(-mean[k], j + 1 < NQ, col(j), T, W, m);
                 v[k][j][0] = f2_add(v[k][j][0], m[0]);
                 v[k][j][1] = f2_add(v[k][j][1], m[1]);
                 t0 = f2_fma(v[k][j][0], v[k][j][0], t0);
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
                 for (int j = 0; j < NQ; ++j) {
                     const f2_t o[2] = {f2_fma(f2_mul(v[k][j][0], q), wv[j][0], bv[j][0]),
                                        f2_fma(f2_mul(v[k][j][1], q), wv[j][1], bv[j][1])};
-                    QY::template store<false>(static_cast<Y *>(a.y) + (row + k) * W, col(j), T, W, o);
+                    QY::store(static_cast<Y *>(a.y) + (row + k) * W, j + 1 < NQ, col(j), T, W, o);
                 }
             }
     }
@@ -608,7 +610,6 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
                                                           in16(a.ds, row * W));
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int n = k < here ? W : 0;
             const f2_t m = f2_both(-mean[k]), q2 = f2_both(rstd[k]);
             q[k] = rstd[k];
             f2_t s0 = f2_both(0.0f), s1 = s0;
@@ -616,8 +617,13 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
             for (int j = 0; j < NQ; ++j) {
                 QX xq;
                 QY gq;
-                xq.template load<false>(xs + k * W, col(j), T, n);
-                gq.template load<false>(gs + k * W, col(j), T, n);
+                if (k == 0 || k < here) {
+                    xq.load(xs + k * W, j + 1 < NQ, col(j), T, W);
+                    gq.load(gs + k * W, j + 1 < NQ, col(j), T, W);
+                } else {
+                    xq.clear();
+                    gq.clear();
+                }
                 xq.pairs(h[k][j]);
                 gq.pairs(g[k][j]);
 #pragma unroll
@@ -672,12 +678,12 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
                     if (a.ds) {
                         QF eq;
                         f2_t t[2];
-                        eq.template load<false>(es + k * W, col(j), T, W);
+                        eq.load(es + k * W, j + 1 < NQ, col(j), T, W);
                         eq.pairs(t);
                         o[0] = f2_add(o[0], t[0]);
                         o[1] = f2_add(o[1], t[1]);
                     }
-                    QF::template store<false>(dxp, col(j), T, W, o);
+                    QF::store(dxp, j + 1 < NQ, col(j), T, W, o);
                 }
             }
     }

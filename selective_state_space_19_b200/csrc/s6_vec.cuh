@@ -68,17 +68,22 @@ struct IoVec {
 // Four elements of a row in one thread, as two float32 pairs.  V = 4: a vector,
 // elements c .. c+3 (c and the row's length multiples of 4, rows aligned to
 // vectors).  V = 1: the elements c, c + S, c + 2S, c + 3S.  Elements from n on
-// are not touched and read as zero; ALL says that there are none.
+// are not touched and read as zero; `all`, a constant where it is used, says that
+// there are none.
 template <typename T, int V>
 struct Quad {
     using Vec = IoVec<T, V>;
     typename Vec::raw r[4 / V];
 
-    template <bool ALL>
-    __device__ __forceinline__ void load(const T *p, int c, int S, int n) {
+    __device__ __forceinline__ void load(const T *p, bool all, int c, int S, int n) {
 #pragma unroll
         for (int i = 0; i < 4 / V; ++i)
-            r[i] = ALL || c + i * S < n ? Vec::load(p + c + i * S) : Vec::zero();
+            r[i] = all || c + i * S < n ? Vec::load(p + c + i * S) : Vec::zero();
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4 / V; ++i)
+            r[i] = Vec::zero();
     }
     __device__ __forceinline__ void pairs(f2_t (&q)[2]) const {
         if constexpr (sizeof(T) == 2 && V == 4) {
@@ -99,18 +104,17 @@ struct Quad {
                 q[i] = f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         }
     }
-    template <bool ALL>
-    static __device__ __forceinline__ void store(T *p, int c, int S, int n, const f2_t (&q)[2]) {
+    static __device__ __forceinline__ void store(T *p, bool all, int c, int S, int n, const f2_t (&q)[2]) {
         float f[4];
         f2_unpack(q[0], f[0], f[1]);
         f2_unpack(q[1], f[2], f[3]);
         if constexpr (V == 4) {
-            if (ALL || c < n)
+            if (all || c < n)
                 Vec::store(p + c, Vec::pack(f));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (ALL || c + i * S < n)
+                if (all || c + i * S < n)
                     p[c + i * S] = io_traits<T>::from_f(f[i]);
         }
     }
@@ -118,8 +122,10 @@ struct Quad {
 
 // A value where the quad's elements are below n, 0 elsewhere.
 template <int V>
-__device__ __forceinline__ void quad_where(float v, int c, int S, int n, f2_t (&q)[2]) {
-    if constexpr (V == 4) {
+__device__ __forceinline__ void quad_where(float v, bool all, int c, int S, int n, f2_t (&q)[2]) {
+    if (all) {
+        q[0] = q[1] = f2_pack(v, v);
+    } else if constexpr (V == 4) {
         q[0] = q[1] = c < n ? f2_pack(v, v) : f2_pack(0.0f, 0.0f);
     } else {
         q[0] = f2_pack(c < n ? v : 0.0f, c + S < n ? v : 0.0f);
