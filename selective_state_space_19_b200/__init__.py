@@ -3,7 +3,7 @@
 This module only marshals arguments: it checks dtype / device / contiguity of
 torch tensors, allocates outputs with torch when the caller passes none, and
 hands raw device pointers plus the current CUDA stream to the C ABI declared in
-``include/s6.h``.  Every arithmetic step runs in the library's CUDA kernels.
+``include/s6.h`` (the training-step calls do this in compiled code, _s6_torch.so).  Every arithmetic step runs in the library's CUDA kernels.
 There is no CPU fallback: if the library is missing, the first call raises.
 
 Functions (same names as the C ABI):
@@ -15,8 +15,6 @@ Functions (same names as the C ABI):
 """
 from __future__ import annotations
 
-import array
-import contextlib
 import ctypes
 import os
 
@@ -480,63 +478,40 @@ def s6_block_step(x, conv_state, h_ssm, w, eps=1e-5, stream=None):
 
 
 # ------------------------------------------------- training-step operators
-# These pass a workspace that torch allocates on the stream of the call, so calls
-# on several streams, and several captured graphs, do not share one.  At small
-# sizes the time of a call is the time of this code: it allocates little and looks
-# at each tensor once.
-_AS_IT_IS = contextlib.nullcontext()
+# These are marshalled by the compiled module _s6_torch (csrc/s6_torch.cpp): it checks the
+# tensors, allocates the outputs and a workspace of the call's own on the stream of the call
+# (so calls on several streams, and several captured graphs, do not share one), and calls
+# the C ABI.
+_native = None
 
 
-def _on(torch, dev, stream):
-    """A context in which ``dev`` is the current device and ``stream`` (None: its
-    current stream) the current stream, for the launch and for what is allocated."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return _AS_IT_IS if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _ext():
+    """The compiled marshalling module (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        lib()
+        _torch()
+        try:
+            from . import _s6_torch
+        except ImportError as e:
+            raise RuntimeError("the module _s6_torch cannot be loaded: build it with"
+                               " `python -m selective_state_space_19_b200._build`") from e
+        _native = _s6_torch
+    return _native
 
 
-def _raw_stream(torch, dev):
-    """The current stream of ``dev`` as the C ABI takes it."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _on(stream, t):
+    """A context in which ``stream`` is the current stream, for the launch and for what is allocated."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
-def _arg(t, name, dtype, shape, dev):
-    """_ptr for a tensor that is as it should be; anything else is left to _ptr to name."""
-    if t is None:
-        return None
-    try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    return _ptr(t, name, dtype, shape, dev)
-
-
-def _workspace(torch, need, where, like):
-    if need < 0:
-        raise S6Error(need, where)
-    return like.new_empty(need, dtype=torch.uint8)
-
-
-def _cuda(torch, t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t
-
-
-def _norm_dims(torch, x, branch, eps, name):
-    """The sizes and types of a LayerNorm of x whose branch side is of type `branch`."""
-    if _cuda(torch, x, "x").dim() < 1:
-        raise ValueError("x must have a last dimension to normalise")
-    xc = _io_code(x)
-    if branch is not x.dtype and branch is not torch.bfloat16:
-        raise TypeError(f"{name} must be {x.dtype}, or bfloat16 beside a float32 x, got {branch}")
-    W = x.shape[-1]
-    return NormDims(x.numel() // W if W else 0, W, xc, xc if branch is x.dtype else S6_BF16, eps)
+def _result(out, where):
+    if type(out) is int:
+        raise S6Error(out, where)
+    return out
 
 
 def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtype=None, want_stats=True,
@@ -547,30 +522,10 @@ def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtyp
     defaults to r's or y's, else to x's.  s: where to put x + r (x itself is allowed).
     Returns (y, s, mean, rstd): s is x when there is no r; mean and rstd [...] float32
     are for s6_layernorm_bwd (None unless want_stats)."""
-    torch = _torch()
-    if y_dtype is None:
-        t = r if r is not None else y if y is not None else x
-        y_dtype = _cuda(torch, t, "r, y or x").dtype
-    if s is not None and r is None:
-        raise ValueError("s is the sum x + r: it needs r")
-    dims = _norm_dims(torch, x, y_dtype, float(eps), "the branch type")
-    shape, dev, f32 = x.shape, x.device, torch.float32
-    width = shape[-1:]
-    mean = rstd = None
-    with _on(torch, dev, stream):
-        if y is None:
-            y = x.new_empty(shape, dtype=y_dtype)
-        if r is not None and s is None:
-            s = x.new_empty(shape)
-        if want_stats:
-            mean = x.new_empty(shape[:-1], dtype=f32)
-            rstd = torch.empty_like(mean)
-        _check(lib().s6_layernorm_fwd(
-            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(r, "r", y_dtype, shape, dev),
-            _arg(w, "w", f32, width, dev), _arg(b, "b", f32, width, dev), _arg(s, "s", x.dtype, shape, dev),
-            _arg(y, "y", y_dtype, shape, dev), mean.data_ptr() if want_stats else None,
-            rstd.data_ptr() if want_stats else None, _raw_stream(torch, dev)), "s6_layernorm_fwd")
-    return y, (x if r is None else s), mean, rstd
+    if stream is not None:
+        with _on(stream, x):
+            return s6_layernorm_fwd(x, w, b, eps, r, s, y, y_dtype, want_stats)
+    return _result((_native or _ext()).layernorm_fwd(x, w, b, eps, r, s, y, y_dtype, want_stats), "s6_layernorm_fwd")
 
 
 def s6_layernorm_bwd(dy, x, mean, rstd, w=None, ds=None, dx=None, want_params=True, stream=None):
@@ -580,25 +535,11 @@ def s6_layernorm_bwd(dy, x, mean, rstd, w=None, ds=None, dx=None, want_params=Tr
     to put the stream's gradient (ds itself is allowed).  Returns a dict of float32
     tensors: dx [..., W] (with respect to s, and so to x and r), dw and db [W] (None
     unless want_params)."""
-    torch = _torch()
-    dims = _norm_dims(torch, x, _cuda(torch, dy, "dy").dtype, 0.0, "dy")
-    shape, dev, f32 = x.shape, x.device, torch.float32
-    rows, width = shape[:-1], shape[-1:]
-    L = lib()
-    dw = db = None
-    with _on(torch, dev, stream):
-        if dx is None:
-            dx = x.new_empty(shape, dtype=f32)
-        if want_params:
-            dw = x.new_empty(width, dtype=f32)
-            db = torch.empty_like(dw)
-        ws = _workspace(torch, L.s6_layernorm_bwd_workspace(ctypes.byref(dims)), "s6_layernorm_bwd", x)
-        _check(L.s6_layernorm_bwd(
-            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(mean, "mean", f32, rows, dev),
-            _arg(rstd, "rstd", f32, rows, dev), _arg(w, "w", f32, width, dev), _arg(dy, "dy", dy.dtype, shape, dev),
-            _arg(ds, "ds", f32, shape, dev), _arg(dx, "dx", f32, shape, dev), dw.data_ptr() if want_params else None,
-            db.data_ptr() if want_params else None, ws.data_ptr(), ws.numel(), _raw_stream(torch, dev)),
-            "s6_layernorm_bwd")
+    if stream is not None:
+        with _on(stream, x):
+            return s6_layernorm_bwd(dy, x, mean, rstd, w, ds, dx, want_params)
+    dx, dw, db = _result((_native or _ext()).layernorm_bwd(dy, x, mean, rstd, w, ds, dx, want_params),
+                         "s6_layernorm_bwd")
     return {"dx": dx, "dw": dw, "db": db}
 
 
@@ -606,102 +547,51 @@ def causal_conv1d_silu_bwd(x, conv_w, dout, conv_b=None, stream=None):
     """Gradients of causal_conv1d_silu_fwd for the loss sum(dout * out): dout [Bt, L, d] is
     float32 (the du of s6_scan_bwd) or x's type.  Returns a dict of float32 tensors: dx
     [Bt, L, d], dconv_w [d, K], dconv_b [d] (None without conv_b)."""
-    torch = _torch()
-    if _cuda(torch, x, "x").dim() != 3:
-        raise ValueError("x must be [batch, seqlen, d_inner]")
-    shape, dev, f32 = x.shape, x.device, torch.float32
-    Bt, L, d = shape
-    K = _cuda(torch, conv_w, "conv_w").shape[-1]
-    gt = _cuda(torch, dout, "dout").dtype
-    if gt is not f32 and gt is not x.dtype:
-        raise TypeError(f"dout must be float32 or {x.dtype}, got {gt}")
-    dims = Dims(Bt, L, d, 1, K, _io_code(x))
-    lb = lib()
-    with _on(torch, dev, stream):
-        dx = x.new_empty(shape, dtype=f32)
-        dw = x.new_empty((d, K), dtype=f32)
-        db = x.new_empty((d,), dtype=f32) if conv_b is not None else None
-        ws = _workspace(torch, lb.causal_conv1d_silu_bwd_workspace(ctypes.byref(dims)), "causal_conv1d_silu_bwd", x)
-        _check(lb.causal_conv1d_silu_bwd(
-            ctypes.byref(dims), _arg(x, "x", x.dtype, shape, dev), _arg(conv_w, "conv_w", f32, (d, K), dev),
-            _arg(conv_b, "conv_b", f32, (d,), dev), _arg(dout, "dout", gt, shape, dev), _io_code(dout),
-            dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), ws.data_ptr(), ws.numel(),
-            _raw_stream(torch, dev)), "causal_conv1d_silu_bwd")
+    if stream is not None:
+        with _on(stream, x):
+            return causal_conv1d_silu_bwd(x, conv_w, dout, conv_b)
+    dx, dw, db = _result((_native or _ext()).conv_bwd(x, conv_w, dout, conv_b), "causal_conv1d_silu_bwd")
     return {"dx": dx, "dconv_w": dw, "dconv_b": db}
 
 
-def _grad_list(torch, grads, norm):
-    """The tensors of a call as what the library reads, (count, and the addresses of the
-    host arrays of pointers, lengths and types), the arrays, and the tensors' device
-    (without tensors that of norm, or the current one)."""
-    T = torch.Tensor
-    if isinstance(grads, T):
-        grads = (grads,)
-    elif isinstance(grads, dict):
-        grads = grads.values()
-    ts = [g for g in grads if g is not None]
-    if norm is not None:
-        if not isinstance(norm, T) or norm.dtype is not torch.float32 or norm.numel() != 1:
-            raise ValueError("norm must be a float32 tensor of 1 element")
-        _ptr(norm, "norm")
-        dev = norm.device
-    elif ts:
-        dev = _cuda(torch, ts[0], "grads[0]").device
-    else:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    codes = {torch.float32: S6_F32, torch.bfloat16: S6_BF16}
-    try:  # three passes in C over a list that is as it should be
-        good = all(map(T.is_contiguous, ts)) and set(map(T.get_device, ts)) <= {dev.index}
-        types = array.array("i", [codes[t.dtype] for t in ts])
-    except (TypeError, KeyError):
-        good = False
-    if not good:
-        for i, t in enumerate(ts):
-            _ptr(t, f"grads[{i}]", device=dev)  # says what is wrong
-        raise TypeError(f"gradients must be float32 or bfloat16, got {sorted({str(t.dtype) for t in ts})}")
-    kept = array.array("q", map(T.data_ptr, ts)), array.array("q", map(T.numel, ts)), types
-    return (len(ts),) + tuple(a.buffer_info()[0] for a in kept), kept, dev
+def _grad_list(grads):
+    """A list of tensors (and None) from what the gradient calls take."""
+    if type(grads) is list:
+        return grads
+    if isinstance(grads, dict):
+        return list(grads.values())
+    return [grads] if isinstance(grads, _torch().Tensor) else list(grads)
 
 
 def s6_grad_norm(grads, norm=None, stream=None):
     """The norm of all gradients taken as one vector: a float32 scalar on the device.
     grads: tensors (a list, or the dict of a backward call; None entries are left out),
     float32 or bfloat16, contiguous, on one device.  norm: where to put it."""
-    torch = _torch()
-    g, kept, dev = _grad_list(torch, grads, norm)
-    L = lib()
-    with _on(torch, dev, stream):
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = _workspace(torch, L.s6_grad_workspace(g[0], g[2]), "s6_grad_norm", norm)
-        _check(L.s6_grad_norm(*g, norm.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(torch, dev)),
-               "s6_grad_norm")
-    return norm
+    grads = _grad_list(grads)
+    if stream is not None:
+        with _on(stream, next((g for g in grads if g is not None), norm)):
+            return s6_grad_norm(grads, norm)
+    return _result((_native or _ext()).grad_norm(grads, norm), "s6_grad_norm")[0]
 
 
 def s6_grad_clip(grads, norm, max_norm, eps=1e-6, stream=None):
     """Scales the gradients in place by min(1, max_norm / (norm + eps)), for a norm that is
     on the device already (one that ranks have combined, say).  No two tensors may overlap."""
-    torch = _torch()
-    g, kept, dev = _grad_list(torch, grads, _cuda(torch, norm, "norm"))
-    with _on(torch, dev, stream):
-        _check(lib().s6_grad_clip(*g, norm.data_ptr(), float(max_norm), float(eps), _raw_stream(torch, dev)),
-               "s6_grad_clip")
+    grads = _grad_list(grads)
+    if stream is not None:
+        with _on(stream, norm):
+            return s6_grad_clip(grads, norm, max_norm, eps)
+    _result((_native or _ext()).grad_clip(grads, norm, max_norm, eps), "s6_grad_clip")
 
 
 def s6_clip_grad_norm(grads, max_norm, eps=1e-6, norm=None, stream=None):
     """s6_grad_norm and s6_grad_clip in one call: scales the gradients in place by
     min(1, max_norm / (norm + eps)) and returns norm, as it was before."""
-    torch = _torch()
-    g, kept, dev = _grad_list(torch, grads, norm)
-    L = lib()
-    with _on(torch, dev, stream):
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = _workspace(torch, L.s6_grad_workspace(g[0], g[2]), "s6_clip_grad_norm", norm)
-        _check(L.s6_clip_grad_norm(*g, float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                                   _raw_stream(torch, dev)), "s6_clip_grad_norm")
-    return norm
+    grads = _grad_list(grads)
+    if stream is not None:
+        with _on(stream, next((g for g in grads if g is not None), norm)):
+            return s6_clip_grad_norm(grads, max_norm, eps, norm)
+    return _result((_native or _ext()).clip_grad_norm(grads, max_norm, eps, norm), "s6_clip_grad_norm")[0]
 
 
 def s6_device_status(stream=None, device=None) -> int:

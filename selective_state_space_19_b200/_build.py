@@ -2,17 +2,20 @@
 
 ``python -m selective_state_space_19_b200._build`` (or ``build()``) compiles the
 ``csrc/*.cu`` files (each includes its kernels), one nvcc process for each, and
-links them into ``libs6_b200.so`` next to this file.  An object file is made
-again when its own sources are newer.  nvcc cross-compiles, so no GPU is needed
-to build.
+links them into ``libs6_b200.so`` next to this file; and ``csrc/s6_torch.cpp``, with
+the host compiler and torch's headers, into the Python module ``_s6_torch.so``,
+which is linked against that library.  An object file is made again when its own
+sources are newer.  nvcc cross-compiles, so no GPU is needed to build.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(CSRC, "obj")
 LIB = os.path.join(HERE, "libs6_b200.so")
+MODULE = os.path.join(HERE, "_s6_torch.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -36,6 +40,7 @@ def _nvcc() -> str:
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(CSRC, "*.cpp")) +
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
@@ -61,23 +66,42 @@ def _fresh(target, sources) -> bool:
 
 
 def up_to_date() -> bool:
-    return _fresh(LIB, _sources())
+    return _fresh(LIB, _sources()) and _fresh(MODULE, _sources())
+
+
+def _module_flags():
+    """Compiler and linker flags for the Python module."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is needed to build _s6_torch.so")
+    torch = spec.submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    compile_ = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *["-I" + d for d in inc]]
+    link = ["-shared", "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch_python", "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
-    tag = ".tmp%d.o" % os.getpid()
-    jobs, objects = [], []
-    for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
-        obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
-        objects.append(obj)
+    tag = ".tmp%d.o" % os.getpid()  # (*.o is ignored by git)
+    cxx = "g++"  # nvcc's host compiler too: the module must share torch's libstdc++, not hold one of its own
+    cxx_flags, cxx_link = _module_flags()
+    jobs, objects = [], {}
+    for src in sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp"))):
+        obj = os.path.splitext(os.path.join(OBJ, os.path.basename(src)))[0] + ".o"
+        objects.setdefault(os.path.splitext(src)[1], []).append(obj)
         if not force and _fresh(obj, _needs(src)):
             continue
-        cmd = [_nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-c", "-o", obj[:-2] + tag, src]
+        out = ["-c", "-o", obj[:-2] + tag, src]
+        cmd = [_nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, *out] if src.endswith(".cu") else [cxx, *cxx_flags, *out]
         if verbose:
-            cmd.insert(1, "-Xptxas=-v")
+            if src.endswith(".cu"):
+                cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), file=sys.stderr)
         jobs.append((subprocess.Popen(cmd), obj, cmd))
     failed = [cmd for p, _, cmd in jobs if p.wait() != 0]
@@ -88,8 +112,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise subprocess.CalledProcessError(1, failed[0])
     for _, obj, _ in jobs:
         os.replace(obj[:-2] + tag, obj)
-    subprocess.check_call([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB + tag, *objects])  # (*.o is ignored by git)
+    subprocess.check_call([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB + tag, *objects[".cu"]])
     os.replace(LIB + tag, LIB)
+    subprocess.check_call([cxx, "-o", MODULE + tag, *objects[".cpp"], *cxx_link])
+    os.replace(MODULE + tag, MODULE)
     return LIB
 
 
