@@ -9,16 +9,20 @@
 //     dx_t = sum_k w_k dv_{t+K-1-k}          (dv = 0 behind the last token)
 //     dw_k = sum_t dv_t x_{t-K+1+k},  dconv_b = sum_t dv_t
 //
-// HBM-bound: x and dout read, dx written.  A thread owns V channels (one
-// vector of every row; a warp covers 32 V consecutive channels) and walks a
-// run of tokens forward, with the last K-1 inputs and the last K-1 dv in
-// registers: the token that completes dv_t also completes dx_{t-K+1}.  A run
-// of tokens [t0, t1) reads K-1 rows before it (inputs only) and K-1 behind it
-// (for the dv that dx of its last tokens needs; these add nothing to dw).
+// HBM-bound: x and dout read, dx written.  A thread owns V channels, a float32
+// pair (a single channel beside a zero where rows do not keep pairs aligned),
+// and walks a run of tokens forward with the last K-1 inputs and the last K-1
+// dv in registers: the token that completes dv_t also completes dx_{t-K+1}.  A
+// run of tokens [t0, t1) reads K-1 rows before it (inputs only) and K-1 behind
+// it (for the dv that dx of its last tokens needs; these add nothing to dw).
 // Rows of the next kConvBwdGroup tokens are in flight while the present ones
-// are worked on, and the arithmetic runs on float32 pairs.  dw and dconv_b stay in registers over all runs of a warp,
-// the block adds its warps up, and s6_sum_parts_kernel adds up the blocks in a
+// are worked on.  dw and dconv_b stay in registers over all runs of a warp, the
+// block adds its warps up, and s6_sum_parts_kernel adds up the blocks in a
 // fixed order.
+//
+// Two channels and groups of 8 tokens against four channels and groups of 4
+// (the registers allow no more): 16x8192x1536 f32 375 and 457 us, with bfloat16
+// x 344 and 352, all bfloat16 327 and 321; 8x256x1536 f32 12.7 and 17.5 us.
 #pragma once
 
 #include <type_traits>
@@ -28,7 +32,7 @@
 namespace s6 {
 
 constexpr int kConvBwdWarps = 4;
-constexpr int kConvBwdGroup = 4;   // tokens of the inner loop, each fetched one group ahead
+constexpr int kConvBwdGroup = 8;   // tokens of the inner loop, each fetched one group ahead
 constexpr int kConvBwdPerSM = 4;   // resident blocks (128 registers a thread)
 
 struct ConvBwdArgs {
@@ -40,14 +44,18 @@ struct ConvBwdArgs {
     float *part;  // [gridDim.y][K + 1][d]
 };
 
-// V channels as float32 pairs (a last odd one beside a zero).
+// V channels as a float32 pair.
 template <typename T, int V>
-__device__ __forceinline__ void conv_pairs(const typename IoVec<T, V>::raw &r, f2_t (&p)[(V + 1) / 2]) {
-    float f[V];
-    IoVec<T, V>::unpack(r, f);
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-        p[i / 2] = f2_pack(f[i], i + 1 < V ? f[i + 1 < V ? i + 1 : i] : 0.0f);
+__device__ __forceinline__ f2_t conv_pair(const typename IoVec<T, V>::raw &r) {
+    if constexpr (V == 1) {
+        float f[1];
+        IoVec<T, 1>::unpack(r, f);
+        return f2_pack(f[0], 0.0f);
+    } else if constexpr (sizeof(T) == 2) {
+        return f2_pack(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    } else {
+        return f2_pack(__uint_as_float(r.x), __uint_as_float(r.y));
+    }
 }
 
 template <typename X, typename G, int V, int K>
@@ -55,7 +63,8 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     using VX = IoVec<X, V>;
     using VG = IoVec<G, V>;
     using VF = IoVec<float, V>;
-    constexpr int H = K - 1, U = kConvBwdGroup, P = (V + 1) / 2;
+    constexpr int H = K - 1, U = kConvBwdGroup;
+    static_assert(V <= 2, "a thread's channels are one pair");
     static_assert(H < U, "the first group of a run holds the tokens that complete no dx of it");
     __shared__ float sums[K + 1][32 * V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -63,23 +72,17 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     const bool live = c < a.d;  // d is a multiple of V
     const int d = a.d, L = a.L;
 
-    f2_t w[K][P], cb[P], dw[K][P], db[P];
     const f2_t zero = f2_pack(0.0f, 0.0f), one = f2_pack(1.0f, 1.0f), minus = f2_pack(-1.0f, -1.0f);
-    {
-        auto param = [&](const float *p, int i, int stride, int at) {
-            return live && p && i < V ? p[static_cast<long long>(c + i) * stride + at] : 0.0f;
-        };
+    auto param = [&](const float *p, int i, int stride, int at) {
+        return live && p && i < V ? p[static_cast<long long>(c + i) * stride + at] : 0.0f;
+    };
+    f2_t w[K], dw[K], db = zero;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                w[k][p] = f2_pack(param(a.conv_w, 2 * p, K, k), param(a.conv_w, 2 * p + 1, K, k));
-                dw[k][p] = zero;
-            }
-            cb[p] = f2_pack(param(a.conv_b, 2 * p, 1, 0), param(a.conv_b, 2 * p + 1, 1, 0));
-            db[p] = zero;
-        }
+    for (int k = 0; k < K; ++k) {
+        w[k] = f2_pack(param(a.conv_w, 0, K, k), param(a.conv_w, 1, K, k));
+        dw[k] = zero;
     }
+    const f2_t cb = f2_pack(param(a.conv_b, 0, 1, 0), param(a.conv_b, 1, 1, 0));
 
     const long long units = static_cast<long long>(a.Bt) * a.runs;
     const long long workers = static_cast<long long>(gridDim.y) * kConvBwdWarps;
@@ -87,24 +90,21 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
         const int b = static_cast<int>(u / a.runs);
         const int t0 = static_cast<int>(u - static_cast<long long>(b) * a.runs) * a.run;
         const int t1 = L - t0 < a.run ? L : t0 + a.run;
-        const int end = t1 + H;                        // steps t0 .. end-1
-        const int rows = end < L ? end : L;            // rows from here on are not read
+        const int end = t1 + H;              // steps t0 .. end-1
+        const int rows = end < L ? end : L;  // rows from here on are not read
         const long long first = (static_cast<long long>(b) * L + t0) * d + c;
-        const X *xp = static_cast<const X *>(a.x) + first;     // row t of the loop, then of its fetches
+        const X *xp = static_cast<const X *>(a.x) + first;  // the next row to be fetched
         const G *gp = static_cast<const G *>(a.dout) + first;
         float *dxp = a.dx + first - static_cast<long long>(H) * d;  // row t - H
 
-        f2_t xw[K][P];  // x_{t-K+1} .. x_t
-        f2_t dv[K][P];  // dv_{t-K+1} .. dv_t
+        f2_t xw[K], dv[K];  // x_{t-K+1} .. x_t and dv_{t-K+1} .. dv_t
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                xw[k][p] = dv[k][p] = zero;
+        for (int k = 0; k < K; ++k)
+            xw[k] = dv[k] = zero;
 #pragma unroll
         for (int k = 0; k < H; ++k)  // x_{t0-K+1} .. x_{t0-1} into slots 1 .. K-1
             if (t0 - H + k >= 0)
-                conv_pairs<X, V>(VX::load(xp - static_cast<long long>(H - k) * d), xw[k + 1]);
+                xw[k + 1] = conv_pair<X, V>(VX::load(xp - static_cast<long long>(H - k) * d));
         typename VX::raw xr[U];
         typename VG::raw gr[U];
 #pragma unroll
@@ -122,51 +122,43 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int tj = t + j;
-                f2_t g[P];
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-#pragma unroll
-                    for (int k = 0; k < H; ++k) {
-                        xw[k][p] = xw[k + 1][p];
-                        dv[k][p] = dv[k + 1][p];
-                    }
-                conv_pairs<X, V>(xr[j], xw[H]);
-                conv_pairs<G, V>(gr[j], g);
+                for (int k = 0; k < H; ++k) {
+                    xw[k] = xw[k + 1];
+                    dv[k] = dv[k + 1];
+                }
+                xw[H] = conv_pair<X, V>(xr[j]);
+                const f2_t g = conv_pair<G, V>(gr[j]);
                 if (!EDGE || tj + U < rows) {
                     xr[j] = VX::load(xp);
                     gr[j] = VG::load(gp);
                 }
                 xp += d;
                 gp += d;
-                float o[2 * P];
+                f2_t v = cb;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    f2_t v = cb[p];
+                for (int k = 0; k < K; ++k)
+                    v = f2_fma(w[k], xw[k], v);
+                float e0, e1, q0, q1;
+                f2_unpack(f2_mul(v, f2_pack(-kLog2e, -kLog2e)), e0, e1);
+                f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), one), q0, q1);
+                const f2_t s = f2_pack(rcp_approx(q0), rcp_approx(q1));
+                dv[H] = f2_mul(g, f2_mul(s, f2_fma(v, f2_fma(s, minus, one), one)));
+                if (EDGE && tj >= L)
+                    dv[H] = zero;
+                if (!EDGE || tj < t1) {
 #pragma unroll
                     for (int k = 0; k < K; ++k)
-                        v = f2_fma(w[k][p], xw[k][p], v);
-                    float e0, e1, q0, q1;
-                    f2_unpack(f2_mul(v, f2_pack(-kLog2e, -kLog2e)), e0, e1);
-                    f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), one), q0, q1);
-                    const f2_t s = f2_pack(rcp_approx(q0), rcp_approx(q1));
-                    const f2_t f = f2_mul(s, f2_fma(v, f2_fma(s, minus, one), one));
-                    dv[H][p] = f2_mul(g[p], f);
-                    if (EDGE && tj >= L)
-                        dv[H][p] = zero;
-                    if (!EDGE || tj < t1) {
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            dw[k][p] = f2_fma(dv[H][p], xw[k][p], dw[k][p]);
-                        db[p] = f2_add(db[p], dv[H][p]);
-                    }
-                    f2_t r = f2_mul(w[0][p], dv[H][p]);
-#pragma unroll
-                    for (int k = 1; k < K; ++k)
-                        r = f2_fma(w[k][p], dv[H - k][p], r);
-                    f2_unpack(r, o[2 * p], o[2 * p + 1]);
+                        dw[k] = f2_fma(dv[H], xw[k], dw[k]);
+                    db = f2_add(db, dv[H]);
                 }
+                f2_t r = f2_mul(w[0], dv[H]);
+#pragma unroll
+                for (int k = 1; k < K; ++k)
+                    r = f2_fma(w[k], dv[H - k], r);
                 if (!EDGE || (tj >= t0 + H && tj < end)) {
-                    float st[V];
+                    float o[2], st[V];
+                    f2_unpack(r, o[0], o[1]);
 #pragma unroll
                     for (int i = 0; i < V; ++i)
                         st[i] = o[i];
@@ -187,17 +179,15 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     for (int s = 0; s < kConvBwdWarps; ++s) {
         if (warp == s) {
 #pragma unroll
-            for (int p = 0; p < P; ++p)
+            for (int k = 0; k <= K; ++k) {
+                float v[2];
+                f2_unpack(k < K ? dw[k < K ? k : 0] : db, v[0], v[1]);
 #pragma unroll
-                for (int k = 0; k <= K; ++k) {
-                    float v[2];
-                    f2_unpack(k < K ? dw[k < K ? k : 0][p] : db[p], v[0], v[1]);
-#pragma unroll
-                    for (int i = 0; i < 2 && 2 * p + i < V; ++i) {
-                        float &at = sums[k][lane * V + 2 * p + i];
-                        at = s ? at + v[i] : v[i];
-                    }
+                for (int i = 0; i < V; ++i) {
+                    float &at = sums[k][lane * V + i];
+                    at = s ? at + v[i] : v[i];
                 }
+            }
         }
         __syncthreads();
     }

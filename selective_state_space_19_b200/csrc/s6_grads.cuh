@@ -4,16 +4,17 @@
 //     n = sqrt(sum over all tensors and elements of g^2)
 //     c = min(1, max_norm / (n + eps)),   g <- c g  where c < 1
 //
-// A list of tensors is cut into chunks of kGradChunkSmall or -Large elements of
-// one tensor each; blocks walk the chunks with a fixed stride, so small and large tensors
-// balance and the order of all additions is fixed.  Pointers and lengths travel
-// in the kernel's parameters: nothing is copied to the device beforehand, and a
-// captured graph holds its own table.
+// A list of tensors is cut into chunks of as many bytes each (the last of a
+// tensor may be shorter), and the blocks walk the chunks with a fixed stride, so
+// small and large tensors balance and the order of all additions is fixed.  (A
+// share of consecutive chunks for each block, which needs no search for the
+// tensor, ran 3 % slower: the blocks' reads lie further apart.)  Pointers and
+// lengths travel in the kernel's parameters: nothing is copied to the device
+// beforehand, and a captured graph holds its own table.
 //
-// Squares are added up in float32 over the 8 elements of one or two loads and
-// in float64 from there.  Where such a group's sum has left the range in which
-// float32 squares are exact to rounding (an overflow, or elements below 1e-15),
-// the group is squared again in float64: the norm holds for every float32.
+// Squares are added up in float32 over 16 elements and in float64 from there.  Where such a sum has left the range in which float32
+// squares are exact to rounding (an overflow, or elements below 1e-12), the
+// elements are squared again in float64: the norm holds for every float32.
 //
 // The second kernel reads the first one's sums (at most kGradMaxBlocks for
 // each 1024 tensors, float64) in every block, in the same order, and scales; it
@@ -25,9 +26,9 @@
 
 namespace s6 {
 
-constexpr int kGradChunkSmall = 4096, kGradChunkLarge = 16384;
+constexpr int kGradChunkStep = 2048, kGradChunkMost = 16384;  // a chunk: a multiple of the one up to the other
 constexpr int kGradThreads = 256;
-constexpr int kGradMaxBlocks = 148 * 6;
+constexpr int kGradMaxBlocks = 148 * 4;
 constexpr int kGradTensors = 1024;  // of one launch; the table is 17 KB of parameters
 constexpr int kGradFew = 96;        // a table for short lists
 
@@ -36,7 +37,7 @@ struct GradTable {
     void *ptr[M];       // bit 0 set: bfloat16
     long long n[M];     // elements
     int end[M];         // chunks of the tensors up to and with this one
-    int tensors, chunks, chunk;  // chunk: elements of one
+    int tensors, chunks, chunk;  // chunk: float32 elements of one; of bfloat16, twice as many
 };
 
 struct GradScaleArgs {
@@ -63,111 +64,102 @@ __device__ __forceinline__ GradSpan grad_span(const GradTable<M> &t, int chunk) 
         else
             lo = mid + 1;
     }
-    const long long at = static_cast<long long>(chunk - (lo ? t.end[lo - 1] : 0)) * t.chunk;
     const uintptr_t raw = reinterpret_cast<uintptr_t>(t.ptr[lo]);
     GradSpan s;
     s.bf16 = raw & 1u;
+    const int most = s.bf16 ? 2 * t.chunk : t.chunk;
+    const long long at = static_cast<long long>(chunk - (lo ? t.end[lo - 1] : 0)) * most;
     s.p = reinterpret_cast<void *>((raw & ~static_cast<uintptr_t>(1)) + at * (s.bf16 ? 2 : 4));
-    s.n = static_cast<int>(t.n[lo] - at < t.chunk ? t.n[lo] - at : t.chunk);
+    s.n = static_cast<int>(t.n[lo] - at < most ? t.n[lo] - at : most);
     return s;
 }
 
-// The sum of squares of 8 elements.  Between 2^-80 and 2^126 the squares that
-// float32 flushed (below 2^-126) are less than 2^-43 of the sum; outside, and
-// for NaN, the elements are taken in float64.  A group of zeros stays here.
-__device__ __forceinline__ double square_sum8(const float (&f)[8]) {
-    float s0 = f[0] * f[0], s1 = f[1] * f[1];
+// The sum of 16 squares, four to an accumulator (6 roundings at most).  Between
+// 2^-80 and 2^126 the squares that float32 flushed (below 2^-126) are less than
+// 2^-42 of the sum; outside, and for NaN, the elements are taken in float64.
+__device__ __forceinline__ double square_sum(const float (&f)[16]) {
+    float q[4];
 #pragma unroll
-    for (int i = 2; i < 8; i += 2) {
-        s0 = fmaf(f[i], f[i], s0);
-        s1 = fmaf(f[i + 1], f[i + 1], s1);
+    for (int i = 0; i < 4; ++i) {
+        q[i] = f[i] * f[i];
+#pragma unroll
+        for (int j = 4; j < 16; j += 4)
+            q[i] = fmaf(f[i + j], f[i + j], q[i]);
     }
-    const float s = s0 + s1;
+    const float s = (q[0] + q[1]) + (q[2] + q[3]);
     if (s >= 0x1p-80f && s <= 0x1p126f)
         return static_cast<double>(s);
     double e = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
         e = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), e);
     return e;
 }
 
-// The part of a chunk whose vectors of 16 bytes are aligned: [head, head + 8 groups) elements.
+// A chunk's aligned vectors of 16 bytes, [head, tail) elements, a warp's next to
+// one another; fewer than a vector's elements lie before and behind them.
 template <typename T>
-__device__ __forceinline__ int grad_head(const T *p, int n) {
-    const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / static_cast<int>(sizeof(T));
-    return head < n ? head : n;
-}
-
-template <typename T>
-__device__ __forceinline__ void grad_load8(const T *p, float (&f)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        float a[4], b[4];
-        const auto r0 = IoVec<T, 4>::load(p), r1 = IoVec<T, 4>::load(p + 4);
-        IoVec<T, 4>::unpack(r0, a);
-        IoVec<T, 4>::unpack(r1, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
-        }
-    } else {
-        IoVec<T, 8>::unpack(IoVec<T, 8>::load(p), f);
+struct GradChunk {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int B = 16 / V;  // vectors that a thread takes together, kGradThreads apart
+    int head, vecs, tail, rest;
+    __device__ __forceinline__ GradChunk(const T *p, int n) {
+        const int h = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) /
+                      static_cast<int>(sizeof(T));
+        head = h < n ? h : n;
+        vecs = (n - head) / V;
+        tail = head + V * vecs;
+        rest = n - V * vecs;
     }
-}
-
-template <typename T>
-__device__ __forceinline__ void grad_store8(T *p, const float (&f)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        float a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = f[i];
-            b[i] = f[4 + i];
-        }
-        IoVec<T, 4>::store(p, IoVec<T, 4>::pack(a));
-        IoVec<T, 4>::store(p + 4, IoVec<T, 4>::pack(b));
-    } else {
-        IoVec<T, 8>::store(p, IoVec<T, 8>::pack(f));
-    }
-}
+    __device__ __forceinline__ int rest_at(int i) const { return i < head ? i : tail + i - head; }
+};
 
 template <typename T>
 __device__ __forceinline__ double chunk_square_sum(const T *p, int n) {
-    const int head = grad_head(p, n), groups = (n - head) >> 3, tail = head + 8 * groups;
+    constexpr int V = GradChunk<T>::V, B = GradChunk<T>::B;
+    using Vec = IoVec<T, V>;
+    const GradChunk<T> c(p, n);
     double s = 0.0;
-#pragma unroll 4
-    for (int k = threadIdx.x; k < groups; k += kGradThreads) {
-        float f[8];
-        grad_load8(p + head + 8 * k, f);
-        s += square_sum8(f);
+#pragma unroll 2
+    for (int k = threadIdx.x; k < c.vecs; k += B * kGradThreads) {
+        float f[16];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int at = k + b * kGradThreads;
+            const typename Vec::raw r = at < c.vecs ? Vec::load(p + c.head + V * at) : Vec::zero();
+            float t[V];
+            Vec::unpack(r, t);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                f[b * V + i] = t[i];
+        }
+        s += square_sum(f);
     }
-    // fewer than 8 elements before the first vector and fewer than 8 behind the last
-    const int rest = head + (n - tail);
-    if (static_cast<int>(threadIdx.x) < rest) {
-        const int i = static_cast<int>(threadIdx.x) < head ? threadIdx.x : tail + threadIdx.x - head;
-        const double v = static_cast<double>(io_traits<T>::to_f(p[i]));
+    if (static_cast<int>(threadIdx.x) < c.rest) {
+        const double v = static_cast<double>(io_traits<T>::to_f(p[c.rest_at(threadIdx.x)]));
         s = fma(v, v, s);
     }
     return s;
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(T *p, int n, float c) {
-    const int head = grad_head(p, n), groups = (n - head) >> 3, tail = head + 8 * groups;
+__device__ __forceinline__ void chunk_scale(T *p, int n, float scale) {
+    constexpr int V = GradChunk<T>::V;
+    using Vec = IoVec<T, V>;
+    const GradChunk<T> c(p, n);
 #pragma unroll 4
-    for (int k = threadIdx.x; k < groups; k += kGradThreads) {
-        float f[8];
-        grad_load8(p + head + 8 * k, f);
+    for (int k = threadIdx.x; k < c.vecs; k += kGradThreads) {
+        T *at = p + c.head + V * k;
+        float f[V];
+        Vec::unpack(Vec::load(at), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] *= c;
-        grad_store8(p + head + 8 * k, f);
+        for (int i = 0; i < V; ++i)
+            f[i] *= scale;
+        Vec::store(at, Vec::pack(f));
     }
-    const int rest = head + (n - tail);
-    if (static_cast<int>(threadIdx.x) < rest) {
-        const int i = static_cast<int>(threadIdx.x) < head ? threadIdx.x : tail + threadIdx.x - head;
-        p[i] = io_traits<T>::from_f(io_traits<T>::to_f(p[i]) * c);
+    if (static_cast<int>(threadIdx.x) < c.rest) {
+        T *at = p + c.rest_at(threadIdx.x);
+        *at = io_traits<T>::from_f(io_traits<T>::to_f(*at) * scale);
     }
 }
 
@@ -185,7 +177,7 @@ __device__ __forceinline__ double grad_block_sum(double v, double *sh) {
 }
 
 template <int M>
-__global__ void __launch_bounds__(kGradThreads, 6) s6_grad_square_kernel(const __grid_constant__ GradTable<M> t,
+__global__ void __launch_bounds__(kGradThreads, 4) s6_grad_square_kernel(const __grid_constant__ GradTable<M> t,
                                                                      double *part) {
     __shared__ double sh[kGradThreads / 32];
     cudaTriggerProgrammaticLaunchCompletion();
@@ -201,7 +193,7 @@ __global__ void __launch_bounds__(kGradThreads, 6) s6_grad_square_kernel(const _
 }
 
 template <int M>
-__global__ void __launch_bounds__(kGradThreads, 6) s6_grad_scale_kernel(const __grid_constant__ GradTable<M> t,
+__global__ void __launch_bounds__(kGradThreads, 4) s6_grad_scale_kernel(const __grid_constant__ GradTable<M> t,
                                                                     const GradScaleArgs a) {
     __shared__ double sh[kGradThreads / 32];
     cudaGridDependencySynchronize();

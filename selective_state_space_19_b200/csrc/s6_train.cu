@@ -287,7 +287,7 @@ struct ConvBwdPlan {
 };
 
 constexpr int64_t kConvBwdBlocks = kSMs * s6::kConvBwdPerSM;
-constexpr int64_t kConvBwdMinRun = 16;        // tokens; shorter runs read more rows twice than they save
+constexpr int64_t kConvBwdMinRun = 8;  // tokens; shorter runs read more rows twice than they save
 
 int64_t conv_bwd_blocks_y(int64_t d, int64_t channels) {
     return std::max<int64_t>(1, kConvBwdBlocks / ceil_div(d, channels));
@@ -332,11 +332,9 @@ int conv_bwd_v(const s6::ConvBwdArgs &in, int64_t K, float *dconv_w, float *dcon
 
 template <typename X, typename G>
 int conv_bwd_io(const s6::ConvBwdArgs &a, int64_t K, float *dconv_w, float *dconv_b, cudaStream_t st) {
-    for (int V = 4; V >= 2; V /= 2)
-        if (a.d % V == 0 && aligned_to(a.x, V * sizeof(X)) && aligned_to(a.dout, V * sizeof(G)) &&
-            aligned_to(a.dx, V * sizeof(float)))
-            return V == 4 ? conv_bwd_v<X, G, 4>(a, K, dconv_w, dconv_b, st)
-                          : conv_bwd_v<X, G, 2>(a, K, dconv_w, dconv_b, st);
+    if (a.d % 2 == 0 && aligned_to(a.x, 2 * sizeof(X)) && aligned_to(a.dout, 2 * sizeof(G)) &&
+        aligned_to(a.dx, 2 * sizeof(float)))
+        return conv_bwd_v<X, G, 2>(a, K, dconv_w, dconv_b, st);
     return conv_bwd_v<X, G, 1>(a, K, dconv_w, dconv_b, st);
 }
 
@@ -350,15 +348,23 @@ int check_conv_bwd_dims(const s6_dims *dims) {
 }
 
 // --------------------------------------------------------------- gradients
-constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^25 of the smaller chunks
+constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^26 of the smallest chunks
 
-// Elements of a chunk: the larger size where even that gives every resident block
-// one, the smaller where the larger would leave SMs without work.
-int grad_chunk(int64_t count, const int64_t *numel) {
+int64_t grad_quads(int64_t numel, int32_t dtype) {  // of 4 bytes
+    return dtype == S6_BF16 ? ceil_div(numel, 2) : numel;
+}
+
+// The size of a chunk (float32 elements; twice as many bfloat16 ones): such that
+// every resident block gets as many as every other, one if they are short, with
+// a chunk set aside for each tensor, whose last one may be a short one.
+int grad_chunk(int64_t count, const int64_t *numel, const int32_t *dtypes) {
     int64_t total = 0;
-    for (int64_t i = 0; i < count && total < kGradMaxNumel; ++i)
-        total += numel[i];
-    return total >= int64_t(s6::kGradMaxBlocks) * s6::kGradChunkLarge ? s6::kGradChunkLarge : s6::kGradChunkSmall;
+    for (int64_t i = 0; i < count; ++i)
+        total += grad_quads(numel[i], dtypes[i]);
+    const int64_t blocks = s6::kGradMaxBlocks, rounds = std::max<int64_t>(1, ceil_div(total, blocks * s6::kGradChunkMost));
+    const int64_t chunks = std::max(blocks * rounds - count, blocks * rounds / 2);
+    const int64_t chunk = ceil_div(ceil_div(total, chunks), s6::kGradChunkStep) * s6::kGradChunkStep;
+    return static_cast<int>(std::min<int64_t>(std::max<int64_t>(chunk, s6::kGradChunkStep), s6::kGradChunkMost));
 }
 
 // Checks a list; `write`: the tensors are written, so no two may share memory.
@@ -406,11 +412,11 @@ template <int M, typename Fn>
 int for_tables(int64_t count, const void *const *grads, const int64_t *numel, const int32_t *dtypes, Fn fn) {
     s6::GradTable<M> t;
     t.tensors = t.chunks = 0;
-    t.chunk = grad_chunk(count, numel);
+    t.chunk = grad_chunk(count, numel, dtypes);
     for (int64_t i = 0; i < count; ++i) {
         if (numel[i] == 0)
             continue;
-        const int chunks = static_cast<int>(ceil_div(numel[i], t.chunk));  // at most 2^25 (check_grads)
+        const int chunks = static_cast<int>(ceil_div(grad_quads(numel[i], dtypes[i]), t.chunk));  // at most 2^26 (check_grads)
         if (t.tensors == M || t.chunks + chunks > (1 << 30)) {
             const int rc = fn(t);
             if (rc != S6_OK)
@@ -612,8 +618,8 @@ int64_t causal_conv1d_silu_bwd_workspace(const s6_dims *dims) {
     const int rc = check_conv_bwd_dims(dims);
     if (rc != S6_OK || dims->batch == 0 || dims->seqlen == 0)
         return rc;
-    // the widest channel tile has the most blocks that share it
-    return conv_bwd_blocks_y(dims->d_inner, 128) * (dims->conv_width + 1) * dims->d_inner *
+    // the wider channel tile has the more blocks that share it
+    return conv_bwd_blocks_y(dims->d_inner, 64) * (dims->conv_width + 1) * dims->d_inner *
            static_cast<int64_t>(sizeof(float));
 }
 
@@ -673,7 +679,7 @@ int64_t s6_grad_workspace(int64_t count, const int64_t *numel) {
             return S6_ERR_INVALID_ARG;
         if (numel[i] > kGradMaxNumel)
             return S6_ERR_UNSUPPORTED;
-        chunks += ceil_div(numel[i], s6::kGradChunkSmall);
+        chunks += ceil_div(numel[i], s6::kGradChunkStep);
     }
     const int64_t launches = count / (count <= s6::kGradFew ? s6::kGradFew : s6::kGradTensors) + 1 + (chunks >> 29);
     return launches * s6::kGradMaxBlocks * static_cast<int64_t>(sizeof(double));
