@@ -16,9 +16,9 @@
 // run of tokens [t0, t1) reads K-1 rows before it (inputs only) and K-1 behind
 // it (for the dv that dx of its last tokens needs; these add nothing to dw).
 // Rows of the next kConvBwdGroup tokens are in flight while the present ones
-// are worked on.  dw and dconv_b stay in registers over all runs of a warp, the
-// block adds its warps up, and s6_sum_parts_kernel adds up the blocks in a
-// fixed order.
+// are worked on.  dw and dconv_b are float32 sums over a run (kConvBwdMaxRun
+// tokens at most) and float64 sums over the runs of a block's warps, which
+// s6_sum_parts_kernel then adds up over the blocks in a fixed order.
 //
 // Two channels and groups of 8 tokens against four channels and groups of 4
 // (the registers allow no more): 16x8192x1536 f32 375 and 457 us, with bfloat16
@@ -34,6 +34,7 @@ namespace s6 {
 constexpr int kConvBwdWarps = 4;
 constexpr int kConvBwdGroup = 8;   // tokens of the inner loop, each fetched one group ahead
 constexpr int kConvBwdPerSM = 4;   // resident blocks (128 registers a thread)
+constexpr int kConvBwdMaxRun = 1024;
 
 struct ConvBwdArgs {
     int Bt, L, d;
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     constexpr int H = K - 1, U = kConvBwdGroup;
     static_assert(V <= 2, "a thread's channels are one pair");
     static_assert(H < U, "the first group of a run holds the tokens that complete no dx of it");
-    __shared__ float sums[K + 1][32 * V];
+    __shared__ double sums[K + 1][V][32 * kConvBwdWarps];  // each thread's own, over its runs
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + lane) * V;
     const bool live = c < a.d;  // d is a multiple of V
@@ -76,13 +77,17 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
     auto param = [&](const float *p, int i, int stride, int at) {
         return live && p && i < V ? p[static_cast<long long>(c + i) * stride + at] : 0.0f;
     };
-    f2_t w[K], dw[K], db = zero;
+    f2_t w[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < K; ++k)
         w[k] = f2_pack(param(a.conv_w, 0, K, k), param(a.conv_w, 1, K, k));
-        dw[k] = zero;
-    }
     const f2_t cb = f2_pack(param(a.conv_b, 0, 1, 0), param(a.conv_b, 1, 1, 0));
+
+#pragma unroll
+    for (int k = 0; k <= K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            sums[k][i][threadIdx.x] = 0.0;
 
     const long long units = static_cast<long long>(a.Bt) * a.runs;
     const long long workers = static_cast<long long>(gridDim.y) * kConvBwdWarps;
@@ -98,9 +103,10 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
         float *dxp = a.dx + first - static_cast<long long>(H) * d;  // row t - H
 
         f2_t xw[K], dv[K];  // x_{t-K+1} .. x_t and dv_{t-K+1} .. dv_t
+        f2_t dw[K], db = zero;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            xw[k] = dv[k] = zero;
+            xw[k] = dv[k] = dw[k] = zero;
 #pragma unroll
         for (int k = 0; k < H; ++k)  // x_{t0-K+1} .. x_{t0-1} into slots 1 .. K-1
             if (t0 - H + k >= 0)
@@ -173,29 +179,28 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, kConvBwdPerSM) s6_conv_sil
             else
                 group(std::true_type{}, t);
         }
+#pragma unroll
+        for (int k = 0; k <= K; ++k) {
+            float v[2];
+            f2_unpack(k < K ? dw[k < K ? k : 0] : db, v[0], v[1]);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                sums[k][i][threadIdx.x] += static_cast<double>(v[i]);
+        }
     }
 
     // the block's warps hold sums of the same channels: add them up in order
-    for (int s = 0; s < kConvBwdWarps; ++s) {
-        if (warp == s) {
-#pragma unroll
-            for (int k = 0; k <= K; ++k) {
-                float v[2];
-                f2_unpack(k < K ? dw[k < K ? k : 0] : db, v[0], v[1]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float &at = sums[k][lane * V + i];
-                    at = s ? at + v[i] : v[i];
-                }
-            }
-        }
-        __syncthreads();
-    }
+    __syncthreads();
     float *part = a.part + static_cast<long long>(blockIdx.y) * (K + 1) * d;
-    for (int i = threadIdx.x; i < (K + 1) * 32 * V; i += 32 * kConvBwdWarps) {
-        const int k = i / (32 * V), j = i - k * 32 * V, ch = blockIdx.x * 32 * V + j;
-        if (ch < d)
-            part[static_cast<long long>(k) * d + ch] = sums[k][j];
+    for (int e = threadIdx.x; e < (K + 1) * 32 * V; e += 32 * kConvBwdWarps) {
+        const int k = e / (32 * V), j = e - k * 32 * V, ch = blockIdx.x * 32 * V + j;
+        if (ch < d) {
+            double s = 0.0;
+#pragma unroll
+            for (int q = 0; q < kConvBwdWarps; ++q)
+                s += sums[k][j % V][32 * q + j / V];
+            part[static_cast<long long>(k) * d + ch] = static_cast<float>(s);
+        }
     }
 }
 

@@ -16,9 +16,9 @@
 // Both are bound by HBM: a row is read once, in the storage type, and
 // everything is computed in float32 from there.  Three forms, by the width:
 //
-//  * up to kNormWarpWidth: a row is one warp's, in its registers.  The warp
-//    walks rows with a fixed stride and fetches the next one while it reduces
-//    the present one.
+//  * up to kNormWarpWidth: a row is one warp's (up to 64 elements 16, 8, 4 or
+//    2 lanes'), in its registers.  The warp walks rows with a fixed stride and
+//    fetches the next one while it reduces the present one.
 //  * up to kNormMaxWidth: rows come through shared memory, copied ahead of
 //    their use without registers, and a block takes two of them at a time.
 //  * above that: the _wide kernels, which read a row more than once.
@@ -66,6 +66,18 @@ struct NormBwdArgs {
     float *part;  // [blocks][2][width]: the block's dw and db; null = neither is wanted
 };
 
+// The sum of v over G neighbouring lanes, in each of them.  Rows of up to 64
+// elements share a warp; its groups may part company at the last rows, so only
+// the group's own lanes take part.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+    const unsigned int mask = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (threadIdx.x & 31 & ~(G - 1));
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(mask, v, o);
+    return v;
+}
+
 // A quad of parameters (all `def` where p is null); 0 from n on.
 template <int V>
 __device__ __forceinline__ void quad_params(const float *p, float def, int c, int S, int n, f2_t (&q)[2]) {
@@ -95,22 +107,23 @@ __device__ __forceinline__ float wide_sum(float v, float *red) {
     return v;
 }
 
-template <typename X, typename Y, int V, int NQ>
+template <typename X, typename Y, int V, int NQ, int G>
 __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * NQ, false) / kNormBlockWarps)
     s6_layernorm_fwd_kernel(const NormFwdArgs a) {
     using QX = Quad<X, V>;
     using QY = Quad<Y, V>;
-    const int lane = threadIdx.x & 31, W = a.width;
-    auto col = [&](int j) { return lane * V + 128 * j; };  // of quad j; only the last can pass the row's end
+    constexpr int kRows = 32 / G * kNormBlockWarps;  // of a block
+    const int lane = threadIdx.x % G, W = a.width;
+    auto col = [&](int j) { return lane * V + 4 * G * j; };  // of quad j; only the last can pass the row's end
     f2_t wv[NQ][2], bv[NQ][2];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-        quad_params<V>(a.w, 1.0f, col(j), 32, W, wv[j]);
-        quad_params<V>(a.b, 0.0f, col(j), 32, W, bv[j]);
+        quad_params<V>(a.w, 1.0f, col(j), G, W, wv[j]);
+        quad_params<V>(a.b, 0.0f, col(j), G, W, bv[j]);
     }
 
-    const long long step = static_cast<long long>(kNormBlockWarps) * gridDim.x;
-    long long row = static_cast<long long>(kNormBlockWarps) * blockIdx.x + (threadIdx.x >> 5);
+    const long long step = static_cast<long long>(kRows) * gridDim.x;
+    long long row = static_cast<long long>(kRows) * blockIdx.x + threadIdx.x / G;
     const X *x = static_cast<const X *>(a.x);
     const Y *r = static_cast<const Y *>(a.r);
     X *s = static_cast<X *>(a.s);
@@ -120,9 +133,9 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
     auto fetch = [&](long long at) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            xr[j].load(x + at * W, j + 1 < NQ, col(j), 32, W);
+            xr[j].load(x + at * W, j + 1 < NQ, col(j), G, W);
             if (r)
-                rr[j].load(r + at * W, j + 1 < NQ, col(j), 32, W);
+                rr[j].load(r + at * W, j + 1 < NQ, col(j), G, W);
         }
     };
     if (row < a.rows)
@@ -138,27 +151,27 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
                 v[j][0] = f2_add(v[j][0], t[0]);
                 v[j][1] = f2_add(v[j][1], t[1]);
                 if (s)
-                    QX::store(s + row * W, j + 1 < NQ, col(j), 32, W, v[j]);
+                    QX::store(s + row * W, j + 1 < NQ, col(j), G, W, v[j]);
             }
             t0 = f2_add(t0, v[j][0]);
             t1 = f2_add(t1, v[j][1]);
         }
         if (row + step < a.rows)
             fetch(row + step);
-        const float mean = warp_sum(f2_sum(t0, t1)) * a.inv_w;
+        const float mean = group_sum<G>(f2_sum(t0, t1)) * a.inv_w;
         // squares of the deviations from the mean, not of the values: a mean that is
         // large next to the deviations costs no digits
         t0 = t1 = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             f2_t m[2];
-            quad_where<V>(-mean, j + 1 < NQ, col(j), 32, W, m);
+            quad_where<V>(-mean, j + 1 < NQ, col(j), G, W, m);
             v[j][0] = f2_add(v[j][0], m[0]);
             v[j][1] = f2_add(v[j][1], m[1]);
             t0 = f2_fma(v[j][0], v[j][0], t0);
             t1 = f2_fma(v[j][1], v[j][1], t1);
         }
-        const float rstd = __frsqrt_rn(warp_sum(f2_sum(t0, t1)) * a.inv_w + a.eps);
+        const float rstd = __frsqrt_rn(group_sum<G>(f2_sum(t0, t1)) * a.inv_w + a.eps);
         if (lane == 0) {
             if (a.mean)
                 a.mean[row] = mean;
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         for (int j = 0; j < NQ; ++j) {
             const f2_t o[2] = {f2_fma(f2_mul(v[j][0], q), wv[j][0], bv[j][0]),
                                f2_fma(f2_mul(v[j][1], q), wv[j][1], bv[j][1])};
-            QY::store(y + row * W, j + 1 < NQ, col(j), 32, W, o);
+            QY::store(y + row * W, j + 1 < NQ, col(j), G, W, o);
         }
     }
 }
@@ -237,23 +250,24 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
 // A lane owns the same columns of every row it meets, so dw and db stay in its
 // registers until the last one; the block then writes one row of partial sums
 // and s6_sum_parts_kernel adds those up.
-template <typename X, typename Y, int V, int NQ>
+template <typename X, typename Y, int V, int NQ, int G>
 __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * NQ, true) / kNormBlockWarps)
     s6_layernorm_bwd_kernel(const NormBwdArgs a) {
     using QX = Quad<X, V>;
     using QY = Quad<Y, V>;
     using QF = Quad<float, V>;
-    const int lane = threadIdx.x & 31, W = a.width;
-    auto col = [&](int j) { return lane * V + 128 * j; };
+    constexpr int kRows = 32 / G * kNormBlockWarps;
+    const int lane = threadIdx.x % G, W = a.width;
+    auto col = [&](int j) { return lane * V + 4 * G * j; };
     f2_t wv[NQ][2], dw[NQ][2], db[NQ][2];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-        quad_params<V>(a.w, 1.0f, col(j), 32, W, wv[j]);
+        quad_params<V>(a.w, 1.0f, col(j), G, W, wv[j]);
         dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = f2_both(0.0f);
     }
 
-    const long long step = static_cast<long long>(kNormBlockWarps) * gridDim.x;
-    long long row = static_cast<long long>(kNormBlockWarps) * blockIdx.x + (threadIdx.x >> 5);
+    const long long step = static_cast<long long>(kRows) * gridDim.x;
+    long long row = static_cast<long long>(kRows) * blockIdx.x + threadIdx.x / G;
     const X *x = static_cast<const X *>(a.x);
     const Y *dy = static_cast<const Y *>(a.dy);
     QX xr[NQ];
@@ -264,8 +278,8 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         rstd = a.rstd[at];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            xr[j].load(x + at * W, j + 1 < NQ, col(j), 32, W);
-            gr[j].load(dy + at * W, j + 1 < NQ, col(j), 32, W);
+            xr[j].load(x + at * W, j + 1 < NQ, col(j), G, W);
+            gr[j].load(dy + at * W, j + 1 < NQ, col(j), G, W);
         }
     };
     if (row < a.rows)
@@ -295,14 +309,19 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         if (a.ds) {
 #pragma unroll
             for (int j = 0; j < NQ; ++j)
-                ds[j].load(a.ds + row * W, j + 1 < NQ, col(j), 32, W);
+                ds[j].load(a.ds + row * W, j + 1 < NQ, col(j), G, W);
         }
         float m0, m1, hi;
         f2_unpack(s0, m0, hi);
         m0 += hi;
         f2_unpack(s1, m1, hi);
         m1 += hi;
-        warp_sum2(m0, m1);
+        if constexpr (G == 32) {
+            warp_sum2(m0, m1);
+        } else {
+            m0 = group_sum<G>(m0);
+            m1 = group_sum<G>(m1);
+        }
         // q (g - m0 - h m1) as q (g - h m1) - q m0
         const f2_t c1 = f2_both(-m1 * a.inv_w), c0 = f2_both(-rq * (m0 * a.inv_w));
 #pragma unroll
@@ -317,32 +336,42 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
                 o[0] = f2_add(o[0], t[0]);
                 o[1] = f2_add(o[1], t[1]);
             }
-            QF::store(a.dx + row * W, j + 1 < NQ, col(j), 32, W, o);
+            QF::store(a.dx + row * W, j + 1 < NQ, col(j), G, W, o);
         }
     }
 
     if (!a.part)
         return;
-    // the block's warps hold sums of the same columns: add them up in order
+    // a warp's groups of lanes hold sums of the same columns, and so do the block's warps:
+    // add them up in order
+#pragma unroll
+    for (int o = G; o < 32; o *= 2)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                dw[j][i] = f2_add(dw[j][i], __shfl_xor_sync(0xffffffffu, dw[j][i], o));
+                db[j][i] = f2_add(db[j][i], __shfl_xor_sync(0xffffffffu, db[j][i], o));
+            }
     __shared__ __align__(16) float sums[2][kNormWarpWidth];
     for (int k = 0; k < kNormBlockWarps; ++k) {
-        if ((threadIdx.x >> 5) == k) {
+        if ((threadIdx.x >> 5) == k && (threadIdx.x & 31) < G) {
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
                 f2_t t[2];
                 Quad<float, V> at;
                 if (k) {
-                    at.load(sums[0], true, col(j), 32, 0);
+                    at.load(sums[0], true, col(j), G, 0);
                     at.pairs(t);
                     dw[j][0] = f2_add(t[0], dw[j][0]);
                     dw[j][1] = f2_add(t[1], dw[j][1]);
-                    at.load(sums[1], true, col(j), 32, 0);
+                    at.load(sums[1], true, col(j), G, 0);
                     at.pairs(t);
                     db[j][0] = f2_add(t[0], db[j][0]);
                     db[j][1] = f2_add(t[1], db[j][1]);
                 }
-                QF::store(sums[0], true, col(j), 32, 0, dw[j]);
-                QF::store(sums[1], true, col(j), 32, 0, db[j]);
+                QF::store(sums[0], true, col(j), G, 0, dw[j]);
+                QF::store(sums[1], true, col(j), G, 0, db[j]);
             }
         }
         __syncthreads();

@@ -81,17 +81,22 @@ int check_norm_dims(const s6_norm_dims *dims) {
     return S6_OK;
 }
 
-// Rows of one warp: as many blocks as are resident, which walk the rows.
+// Rows of one warp or of some lanes: as many blocks as are resident, which walk the
+// rows.
 struct NormWarpPlan {
     int elems;  // elements of a row that a lane holds, at most
+    int lanes;  // of a row: 32, or with 4 elements a lane the fewest that hold it, 2 at least
     int64_t blocks;
 };
 
 NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd) {
     NormWarpPlan p;
     p.elems = static_cast<int>(4 * ceil_div(width, 128));
-    p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps),
-                        kSMs * s6::norm_warps_resident(p.elems, bwd) / s6::kNormBlockWarps);
+    p.lanes = 32;
+    while (p.lanes > 2 && 4 * (p.lanes / 2) >= width)
+        p.lanes /= 2;
+    const int64_t block_rows = s6::kNormBlockWarps * (32 / p.lanes);
+    p.blocks = std::min(ceil_div(rows, block_rows), kSMs * s6::norm_warps_resident(p.elems, bwd) / s6::kNormBlockWarps);
     return p;
 }
 
@@ -138,28 +143,36 @@ int64_t norm_wide_runs(int64_t rows, int64_t width) {
     return std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
 }
 
-template <typename X, typename Y, int V, int NQ>
+template <typename X, typename Y, int V, int NQ, int G>
 void norm_launch(const s6::NormFwdArgs &a, unsigned grid, cudaStream_t st) {
-    s6::s6_layernorm_fwd_kernel<X, Y, V, NQ><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
+    s6::s6_layernorm_fwd_kernel<X, Y, V, NQ, G><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
 }
 
-template <typename X, typename Y, int V, int NQ>
+template <typename X, typename Y, int V, int NQ, int G>
 void norm_launch(const s6::NormBwdArgs &a, unsigned grid, cudaStream_t st) {
-    s6::s6_layernorm_bwd_kernel<X, Y, V, NQ><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
+    s6::s6_layernorm_bwd_kernel<X, Y, V, NQ, G><<<grid, 32 * s6::kNormBlockWarps, 0, st>>>(a);
 }
 
-// Rows of one warp: the instantiation that holds p.elems elements a lane.
+// The instantiation that holds p.elems elements a lane on p.lanes lanes.
 template <typename X, typename Y, int V, typename Args>
 int norm_warp_rows(const Args &a, const NormWarpPlan &p, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(p.blocks);
-    if (p.elems <= 4)
-        norm_launch<X, Y, V, 1>(a, grid, st);
+    if (p.lanes == 2)
+        norm_launch<X, Y, V, 1, 2>(a, grid, st);
+    else if (p.lanes == 4)
+        norm_launch<X, Y, V, 1, 4>(a, grid, st);
+    else if (p.lanes == 8)
+        norm_launch<X, Y, V, 1, 8>(a, grid, st);
+    else if (p.lanes == 16)
+        norm_launch<X, Y, V, 1, 16>(a, grid, st);
+    else if (p.elems <= 4)
+        norm_launch<X, Y, V, 1, 32>(a, grid, st);
     else if (p.elems <= 8)
-        norm_launch<X, Y, V, 2>(a, grid, st);
+        norm_launch<X, Y, V, 2, 32>(a, grid, st);
     else if (p.elems <= 12)
-        norm_launch<X, Y, V, 3>(a, grid, st);
+        norm_launch<X, Y, V, 3, 32>(a, grid, st);
     else
-        norm_launch<X, Y, V, 4>(a, grid, st);
+        norm_launch<X, Y, V, 4, 32>(a, grid, st);
     return launch_status(cudaGetLastError());
 }
 
@@ -293,14 +306,16 @@ int64_t conv_bwd_blocks_y(int64_t d, int64_t channels) {
     return std::max<int64_t>(1, kConvBwdBlocks / ceil_div(d, channels));
 }
 
-// One run of tokens for each warp where the warps outnumber the sequences, else
-// about four, so that the last ones to finish are short.
+// Runs that share the tokens out evenly, as many for each warp as every other: one
+// where the warps outnumber the sequences, else about four in all, and more where
+// they would be longer than kConvBwdMaxRun.
 ConvBwdPlan conv_bwd_plan(int64_t Bt, int64_t L, int64_t d, int V) {
     ConvBwdPlan p;
     p.tiles = ceil_div(d, 32 * V);
     p.blocks_y = conv_bwd_blocks_y(d, 32 * V);
     const int64_t warps = p.blocks_y * s6::kConvBwdWarps;
-    const int64_t want = Bt < warps ? warps / Bt : ceil_div(4 * warps, Bt);
+    int64_t want = Bt < warps ? warps / Bt : ceil_div(4 * warps, Bt);  // runs of a sequence
+    want *= ceil_div(ceil_div(L, want), static_cast<int64_t>(s6::kConvBwdMaxRun));
     p.run = std::max(ceil_div(L, want), std::min(L, kConvBwdMinRun));
     p.runs = ceil_div(L, p.run);
     p.blocks_y = std::min(p.blocks_y, ceil_div(Bt * p.runs, s6::kConvBwdWarps));

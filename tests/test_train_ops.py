@@ -47,7 +47,7 @@ def _f64(t):
 TYPES = [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")]
 # one row and one column, a part of a warp, every count of vectors a thread holds, the border to several warps,
 # odd widths on each side of it, and the widest rows with their wide form
-SHAPES = [(1, 1), (3, 2), (5, 8), (1, 384), (300, 384), (9, 130), (37, 500), (2, 512), (4, 513), (3, 516),
+SHAPES = [(1, 1), (3, 2), (5, 8), (67, 7), (131, 9), (45, 16), (33, 31), (70, 33), (9, 64), (13, 65), (30001, 12), (1, 384), (300, 384), (9, 130), (37, 500), (2, 512), (4, 513), (3, 516),
           (21, 1001), (33, 1536), (2500, 64), (5, 2560), (3, 2561), (2, 8192), (2, 8191), (2, 8196), (3, 8193),
           (1, 20000), (7001, 516), (2500, 1031), (1300, 2568)]
 
