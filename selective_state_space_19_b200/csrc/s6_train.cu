@@ -108,9 +108,20 @@ struct NormBlockPlan {
 };
 
 constexpr int kSmemSM = 227 * 1024, kSmemBlock = 2 * 1024;  // of an SM; a block's other shared memory, at most
-constexpr int norm_block_per_sm(int threads, bool bwd) {    // by the registers (the kernels' launch bounds)
+constexpr int norm_block_per_sm(int threads, bool bwd) {    // by the registers
     return bwd ? 512 / threads : threads == 512 ? 1 : 768 / threads;
 }
+// The kernels' launch bound.  The forward with three quads comes out at 72 to 80
+// registers, which is what norm_block_per_sm counts on, under the bound of two
+// thirds of its blocks; held to that number it spills.
+constexpr int norm_block_bound(int threads, int quads, bool bwd) {
+    return !bwd && quads == 3 ? 512 / threads : norm_block_per_sm(threads, bwd);
+}
+
+// Quads of a thread up to which it holds two rows at once: beside its parameters'
+// sums the backward spills with three (8192x2560 f32 54 us with two rows, 47 with
+// one; 6000x5120 88 and 66).
+constexpr int norm_two_rows_quads(bool bwd) { return bwd ? 2 : 3; }
 
 // Two rows a step where two steps of them fit in shared memory beside at least
 // three quarters of the blocks that the registers allow, else one.  `row_bytes`:
@@ -123,7 +134,7 @@ NormBlockPlan norm_block_plan(int64_t rows, int64_t width, int64_t row_bytes, bo
     auto fits = [&](int64_t r) {  // blocks with two stages of r rows (16 bytes a tensor beside them)
         return static_cast<int>(kSmemSM / (2 * (r * row_bytes + 96) + kSmemBlock));
     };
-    p.rows = p.quads <= 3 && 4 * std::min(most, fits(2)) >= 3 * most ? 2 : 1;
+    p.rows = p.quads <= norm_two_rows_quads(bwd) && 4 * std::min(most, fits(2)) >= 3 * most ? 2 : 1;
     p.per_sm = std::min(most, std::max(1, fits(p.rows)));
     p.blocks = std::min(ceil_div(rows, p.rows), kSMs * p.per_sm);
     return p;
@@ -178,11 +189,11 @@ int norm_warp_rows(const Args &a, const NormWarpPlan &p, cudaStream_t st) {
 
 template <typename X, typename Y, int V, int NQ, int R, int T>
 auto norm_block_kernel(const s6::NormFwdBlockArgs &) {
-    return s6::s6_layernorm_fwd_block_kernel<X, Y, V, NQ, R, T, norm_block_per_sm(T, false)>;
+    return s6::s6_layernorm_fwd_block_kernel<X, Y, V, NQ, R, T, norm_block_bound(T, NQ, false)>;
 }
 template <typename X, typename Y, int V, int NQ, int R, int T>
 auto norm_block_kernel(const s6::NormBwdBlockArgs &) {
-    return s6::s6_layernorm_bwd_block_kernel<X, Y, V, NQ, R, T, norm_block_per_sm(T, true)>;
+    return s6::s6_layernorm_bwd_block_kernel<X, Y, V, NQ, R, T, norm_block_bound(T, NQ, true)>;
 }
 
 // Launches with more dynamic shared memory than the default 48 KB (the attribute
@@ -199,8 +210,10 @@ int norm_block_launch(const Args &a, const NormBlockPlan &p, int smem, cudaStrea
 
 template <typename X, typename Y, int V, int NQ, int T, typename Args>
 int norm_block_r(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
-    return p.rows == 1 ? norm_block_launch<X, Y, V, NQ, 1, T>(a, p, smem, st)
-                       : norm_block_launch<X, Y, V, NQ, 2, T>(a, p, smem, st);
+    if constexpr (NQ <= norm_two_rows_quads(std::is_same<Args, s6::NormBwdBlockArgs>::value))
+        if (p.rows == 2)
+            return norm_block_launch<X, Y, V, NQ, 2, T>(a, p, smem, st);
+    return norm_block_launch<X, Y, V, NQ, 1, T>(a, p, smem, st);
 }
 
 // 2 or 3 quads of 128, 256 or 512 threads, and 4 of 512 (norm_block_plan).
@@ -214,7 +227,7 @@ int norm_block_rows(const Args &a, const NormBlockPlan &p, int smem, cudaStream_
                             : norm_block_r<X, Y, V, 3, 256>(a, p, smem, st);
     return p.quads == 2   ? norm_block_r<X, Y, V, 2, 512>(a, p, smem, st)
            : p.quads == 3 ? norm_block_r<X, Y, V, 3, 512>(a, p, smem, st)
-                          : norm_block_launch<X, Y, V, 4, 1, 512>(a, p, smem, st);
+                          : norm_block_r<X, Y, V, 4, 512>(a, p, smem, st);
 }
 
 template <typename X, typename Y, int V>
