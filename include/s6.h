@@ -544,7 +544,8 @@ S6_API int causal_conv1d_silu_bwd(const s6_dims *dims, const void *x, const floa
  *  max_norm finite, >= 0;  eps finite, >= 0
  *
  * The norm holds over float32's whole range: squares do not overflow or vanish
- * (a norm above the largest float32 is inf).  Where c is 1 nothing is written.
+ * (a norm above the largest float32 is inf).  Where c is 1 or norm is 0 nothing
+ * is written.
  * An infinite norm gives c = 0, which turns finite gradients into 0 and
  * infinite ones into NaN; a NaN norm turns all of them into NaN.
  */

@@ -208,9 +208,10 @@ __global__ void __launch_bounds__(kGradThreads, 4) s6_grad_scale_kernel(const __
     }
     if (a.norm_out && blockIdx.x == 0 && threadIdx.x == 0)
         *a.norm_out = norm;
-    // a NaN norm makes c NaN, and every gradient with it; an infinite one makes it 0
+    // a NaN norm makes c NaN, and every gradient with it; an infinite one makes it 0; gradients
+    // that are all zero stay so, with a bound and an eps of 0 too (c is 0 / 0 then)
     const float c = a.max_norm / (norm + a.eps);
-    if (c >= 1.0f)
+    if (c >= 1.0f || norm == 0.0f)
         return;
     for (int k = t.chunks - 1 - static_cast<int>(blockIdx.x); k >= 0; k -= gridDim.x) {
         const GradSpan g = grad_span(t, k);

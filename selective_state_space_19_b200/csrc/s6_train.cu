@@ -108,29 +108,29 @@ struct NormBlockPlan {
 };
 
 constexpr int kSmemSM = 227 * 1024, kSmemBlock = 2 * 1024;  // of an SM; a block's other shared memory, at most
-constexpr int norm_block_per_sm(int threads, bool bwd) {    // by the registers
-    return bwd ? 512 / threads : threads == 512 ? 1 : 768 / threads;
+// by the registers: 128 a thread backward; forward 96 with four quads and 80 with fewer
+constexpr int norm_block_per_sm(int threads, int quads, bool bwd) {
+    return bwd ? 512 / threads : threads == 512 ? 1 : (quads == 4 ? 640 : 768) / threads;
 }
-// The kernels' launch bound.  The forward with three quads comes out at 72 to 80
-// registers, which is what norm_block_per_sm counts on, under the bound of two
-// thirds of its blocks; held to that number it spills.
+// The kernels' launch bound.  The forward comes out at what norm_block_per_sm counts
+// on under the bound of 128 registers; held to that number it spills.
 constexpr int norm_block_bound(int threads, int quads, bool bwd) {
-    return !bwd && quads == 3 ? 512 / threads : norm_block_per_sm(threads, bwd);
+    return !bwd && quads >= 3 ? 512 / threads : norm_block_per_sm(threads, quads, bwd);
 }
 
 // Quads of a thread up to which it holds two rows at once: beside its parameters'
 // sums the backward spills with three (8192x2560 f32 54 us with two rows, 47 with
 // one; 6000x5120 88 and 66).
-constexpr int norm_two_rows_quads(bool bwd) { return bwd ? 2 : 3; }
+constexpr int norm_two_rows_quads(bool bwd) { return bwd ? 2 : 4; }
 
 // Two rows a step where two steps of them fit in shared memory beside at least
 // three quarters of the blocks that the registers allow, else one.  `row_bytes`:
 // what a row takes of all tensors.
 NormBlockPlan norm_block_plan(int64_t rows, int64_t width, int64_t row_bytes, bool bwd) {
     NormBlockPlan p;
-    p.threads = width <= 12 * 128 ? 128 : width <= 12 * 256 ? 256 : 512;
+    p.threads = width <= 16 * 128 ? 128 : width <= 16 * 256 ? 256 : 512;
     p.quads = static_cast<int>(std::max<int64_t>(2, ceil_div(width, 4 * p.threads)));
-    const int most = norm_block_per_sm(p.threads, bwd);
+    const int most = norm_block_per_sm(p.threads, p.quads, bwd);
     auto fits = [&](int64_t r) {  // blocks with two stages of r rows (16 bytes a tensor beside them)
         return static_cast<int>(kSmemSM / (2 * (r * row_bytes + 96) + kSmemBlock));
     };
@@ -216,18 +216,18 @@ int norm_block_r(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t s
     return norm_block_launch<X, Y, V, NQ, 1, T>(a, p, smem, st);
 }
 
-// 2 or 3 quads of 128, 256 or 512 threads, and 4 of 512 (norm_block_plan).
+// 2 to 4 quads of 128 threads, 3 or 4 of 256 or 512 (norm_block_plan).
 template <typename X, typename Y, int V, typename Args>
 int norm_block_rows(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
     if (p.threads == 128)
-        return p.quads == 2 ? norm_block_r<X, Y, V, 2, 128>(a, p, smem, st)
-                            : norm_block_r<X, Y, V, 3, 128>(a, p, smem, st);
+        return p.quads == 2   ? norm_block_r<X, Y, V, 2, 128>(a, p, smem, st)
+               : p.quads == 3 ? norm_block_r<X, Y, V, 3, 128>(a, p, smem, st)
+                              : norm_block_r<X, Y, V, 4, 128>(a, p, smem, st);
     if (p.threads == 256)
-        return p.quads == 2 ? norm_block_r<X, Y, V, 2, 256>(a, p, smem, st)
-                            : norm_block_r<X, Y, V, 3, 256>(a, p, smem, st);
-    return p.quads == 2   ? norm_block_r<X, Y, V, 2, 512>(a, p, smem, st)
-           : p.quads == 3 ? norm_block_r<X, Y, V, 3, 512>(a, p, smem, st)
-                          : norm_block_r<X, Y, V, 4, 512>(a, p, smem, st);
+        return p.quads == 3 ? norm_block_r<X, Y, V, 3, 256>(a, p, smem, st)
+                            : norm_block_r<X, Y, V, 4, 256>(a, p, smem, st);
+    return p.quads == 3 ? norm_block_r<X, Y, V, 3, 512>(a, p, smem, st)
+                        : norm_block_r<X, Y, V, 4, 512>(a, p, smem, st);
 }
 
 template <typename X, typename Y, int V>

@@ -511,6 +511,67 @@ def test_captured_and_replayed_in_two_graphs():
             assert all(torch.equal(p, q) for p, q in zip(c, grads)), turn
 
 
+@pytest.mark.parametrize("W", [40, 1000, 1536, 8192, 9001])
+def test_every_form_of_the_layernorm_captured(W):
+    """Rows of some lanes, of a block through shared memory and of several walks, in one
+    graph and on a second stream, without an earlier call."""
+    import torch
+    import selective_state_space_19_b200 as S
+    run, inputs, grads = _calls(S, W, rows=700, W=W)
+    keep = [g.clone() for g in grads]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    side = torch.cuda.Stream()
+    for turn in range(2):
+        for t in inputs:
+            t.normal_()
+        results = []
+        for how in ("replay", "call", "stream"):
+            for g, o in zip(grads, keep):
+                g.copy_(o)
+            torch.cuda.synchronize()
+            if how == "replay":
+                graph.replay()
+                torch.cuda.synchronize()
+                results.append([t.clone() for t in out])
+            else:
+                results.append(run(stream=side if how == "stream" else None))
+                torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for r in results[1:] for p, q in zip(r, results[0]))
+
+
+def test_gradients_of_zero_stay_zero_whatever_the_bound():
+    import torch
+    import selective_state_space_19_b200 as S
+    z = torch.zeros(300, device="cuda")
+    for max_norm, eps in ((0.0, 0.0), (0.0, 1e-6), (1.0, 0.0)):
+        assert S.s6_clip_grad_norm([z], max_norm, eps=eps).item() == 0.0
+        assert torch.equal(z, torch.zeros_like(z))
+
+
+def test_layernorm_result_does_not_depend_on_the_rows_around_it():
+    """A row gives the same bits alone, in a batch and at another place in it."""
+    import torch
+    import selective_state_space_19_b200 as S
+    for W in (33, 384, 1001, 2560, 8191):
+        for t in (torch.float32, torch.bfloat16):
+            x = torch.randn(37, W, device="cuda").to(t)
+            dy = torch.randn(37, W, device="cuda").to(t)
+            y, _, mean, rstd = S.s6_layernorm_fwd(x)
+            dx = S.s6_layernorm_bwd(dy, x, mean, rstd)["dx"]
+            for first in (0, 1, 8, 36):
+                part = x[first:].clone()
+                y2, _, m2, r2 = S.s6_layernorm_fwd(part)
+                dx2 = S.s6_layernorm_bwd(dy[first:].clone(), part, m2, r2)["dx"]
+                assert torch.equal(y2, y[first:]) and torch.equal(m2, mean[first:]) and torch.equal(dx2, dx[first:])
+
+
+def test_no_bounded_wait_gave_up():
+    import selective_state_space_19_b200 as S
+    assert S.s6_device_status() == 0
+
+
 def test_stream_of_another_device_is_refused():
     import torch
     import selective_state_space_19_b200 as S
