@@ -12,14 +12,22 @@
 // lengths travel in the kernel's parameters: nothing is copied to the device
 // beforehand, and a captured graph holds its own table.
 //
-// Squares are added up in float32 over 16 elements and in float64 from there.  Where such a sum has left the range in which float32
-// squares are exact to rounding (an overflow, or elements below 1e-12), the
-// elements are squared again in float64: the norm holds for every float32.
+// Squares are added up in float32 over 16 elements and in float64 from there.
+// Where such a sum has left the range in which float32 squares are exact to
+// rounding (an overflow, or elements below 1e-12), the elements are squared
+// again in float64: the norm holds for every float32.
 //
 // The second kernel reads the first one's sums (at most kGradMaxBlocks for
 // each 1024 tensors, float64) in every block, in the same order, and scales; it
 // walks the chunks from the last to the first, as the last ones read are the
-// likeliest to be in L2 still.  Nothing is written where c is 1.
+// likeliest to be in L2 still.  Nothing is written where c is 1 or n is 0.
+//
+// Bound by memory: the gradients are read twice and written once, the second
+// read from L2 where they fit.  Measured on one B200 (copies run at 6,521 GB/s):
+// 66 tensors of 46 MB 27 us; 132 tensors of 1 GB 486 us, where reading twice and
+// writing takes 456.  One 16-byte vector a thread, a warp's next to one another:
+// two neighbouring ones left each access with half-used sectors (31 us for the
+// 66 tensors).  Four blocks an SM against six and eight: 486, 500, 497 us.
 #pragma once
 
 #include "s6_vec.cuh"
@@ -29,7 +37,7 @@ namespace s6 {
 constexpr int kGradChunkStep = 2048, kGradChunkMost = 16384;  // a chunk: a multiple of the one up to the other
 constexpr int kGradThreads = 256;
 constexpr int kGradMaxBlocks = 148 * 4;
-constexpr int kGradTensors = 1024;  // of one launch; the table is 17 KB of parameters
+constexpr int kGradTensors = 1024;  // of one launch; the table is 20 KB of parameters
 constexpr int kGradFew = 96;        // a table for short lists
 
 template <int M>
