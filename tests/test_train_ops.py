@@ -567,6 +567,57 @@ def test_layernorm_result_does_not_depend_on_the_rows_around_it():
                 assert torch.equal(y2, y[first:]) and torch.equal(m2, mean[first:]) and torch.equal(dx2, dx[first:])
 
 
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows, tokens and elements equal those of a
+    small call on the same values."""
+    import torch
+    import selective_state_space_19_b200 as S
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    bf = torch.bfloat16
+    for rows, W in ((5_700_000, 384), (840_000, 2561), (240_000, 9001)):  # a form of the kernels each
+        x, dy = torch.empty(rows, W, device="cuda", dtype=bf), torch.empty(rows, W, device="cuda", dtype=bf)
+        assert x.numel() > 1 << 31
+        x.normal_()
+        dy.normal_()
+        y, _, mean, rstd = S.s6_layernorm_fwd(x)
+        y2, _, m2, r2 = S.s6_layernorm_fwd(x[-50:].clone())
+        assert torch.equal(y[-50:], y2) and torch.equal(mean[-50:], m2) and torch.equal(rstd[-50:], r2)
+        del y
+        dx = S.s6_layernorm_bwd(dy, x, mean, rstd)["dx"]
+        assert torch.equal(dx[-50:], S.s6_layernorm_bwd(dy[-50:].clone(), x[-50:].clone(), m2, r2)["dx"])
+        del x, dy, dx
+    x = torch.randn(3, 650_000, 1102, device="cuda", dtype=bf)
+    w = torch.randn(1102, 4, device="cuda")
+    assert x.numel() > 1 << 31
+    dx = S.causal_conv1d_silu_bwd(x, w, x)["dx"]
+    tail = x[2:, -64:].clone()
+    assert torch.equal(dx[2:, -60:], S.causal_conv1d_silu_bwd(tail, w, tail)["dx"][:, -60:])
+    del dx, tail
+    flat = x.view(-1)
+    flat.fill_(0.0)
+    flat[-1], flat[5], flat[(1 << 31) + 3] = 3.0, 4.0, 12.0
+    assert S.s6_clip_grad_norm([flat], 6.5, eps=0.0).item() == 13.0
+    assert flat[-1].item() == 1.5 and flat[5].item() == 2.0 and flat[(1 << 31) + 3].item() == 6.0
+
+
+def test_the_c_call_without_the_optional_outputs():
+    """The C ABI's own freedom: a sum that is not stored, statistics that are not wanted."""
+    import ctypes
+    import torch
+    import selective_state_space_19_b200 as S
+    for W in (40, 1536, 9000):
+        x, r = torch.randn(9, W, device="cuda"), torch.randn(9, W, device="cuda")
+        want = S.s6_layernorm_fwd(x, r=r)[0]
+        keep = x.clone()
+        y = torch.empty_like(x)
+        dims = S.NormDims(9, W, S.S6_F32, S.S6_F32, 1e-5)
+        st = S.lib().s6_layernorm_fwd(ctypes.byref(dims), x.data_ptr(), r.data_ptr(), None, None, None, y.data_ptr(),
+                                      None, None, torch.cuda.current_stream().cuda_stream)
+        assert st == S.S6_OK and torch.equal(y, want) and torch.equal(x, keep)
+
+
 def test_no_bounded_wait_gave_up():
     import selective_state_space_19_b200 as S
     assert S.s6_device_status() == 0
