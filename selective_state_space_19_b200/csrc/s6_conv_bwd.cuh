@@ -36,7 +36,7 @@ namespace s6 {
 constexpr int kConvBwdWarps = 4;
 constexpr int kConvBwdGroup = 8;   // tokens of the inner loop, each fetched one group ahead
 constexpr int kConvBwdPerSM = 4;   // resident blocks (128 registers a thread)
-constexpr int kConvBwdMaxRun = 1536;  // tokens that float32 sums run over: off by 7e-7 of the result at that length
+constexpr int kConvBwdMaxRun = 1024;  // tokens that float32 sums run over: off by 6e-7 of the result at that length
 
 struct ConvBwdArgs {
     int Bt, L, d;
