@@ -24,7 +24,7 @@
 //  * above that: the _wide kernels, which read a row more than once.
 //
 // Measured on one B200 (copies run at 6,521 GB/s): 131072 rows of 384, a float32
-// stream and a bfloat16 branch: forward with the add 106 us = 88 % of the copy
+// stream and a bfloat16 branch: forward with the add 99 us = 94 % of the copy
 // rate, backward with the residual gradient 112 us = 96 %.  Wide rows: 8192x2560
 // f32 33 us forward and 47 backward (78, 82 %), bfloat16 21 and 41 (61, 63 %:
 // bound by issue, 18 and 30 instructions an element), 8191x2561 bfloat16 25.

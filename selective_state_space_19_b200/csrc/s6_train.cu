@@ -89,14 +89,24 @@ struct NormWarpPlan {
     int64_t blocks;
 };
 
-NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd) {
+// `read`: bytes of a row that the forward reads where it also adds (0: it does not).
+// Four streams of reads and writes are fastest with about 38 KB of reads in flight
+// on an SM: 131072x384 f32 + f32 139 us with 20 warps (61 KB), 137 with 16, 132 with 12;
+// f32 + bfloat16 106 with 20 (46 KB), 98 with 16, 109 with 12; bfloat16 71, 77, 85
+// (31 KB with 20).  Without the add more warps are faster throughout.
+constexpr int64_t kNormAddReads = 38 * 1024;
+
+NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd, int64_t read = 0) {
     NormWarpPlan p;
     p.elems = static_cast<int>(4 * ceil_div(width, 128));
     p.lanes = 32;
     while (p.lanes > 2 && 4 * (p.lanes / 2) >= width)
         p.lanes /= 2;
-    const int64_t block_rows = s6::kNormBlockWarps * (32 / p.lanes);
-    p.blocks = std::min(ceil_div(rows, block_rows), kSMs * s6::norm_warps_resident(p.elems, bwd) / s6::kNormBlockWarps);
+    const int64_t warp_rows = 32 / p.lanes;
+    int64_t warps = s6::norm_warps_resident(p.elems, bwd);
+    if (read)
+        warps = std::min(warps, std::max<int64_t>(s6::kNormBlockWarps, kNormAddReads / (read * warp_rows)));
+    p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps * warp_rows), kSMs * warps / s6::kNormBlockWarps);
     return p;
 }
 
@@ -239,7 +249,8 @@ int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
         return launch_status(cudaGetLastError());
     }
     if (a.width <= s6::kNormWarpWidth)
-        return norm_warp_rows<X, Y, V>(a, norm_warp_plan(a.rows, a.width, false), st);
+        return norm_warp_rows<X, Y, V>(
+            a, norm_warp_plan(a.rows, a.width, false, a.r ? a.width * int64_t(sizeof(X) + sizeof(Y)) : 0), st);
     const int64_t sx = sizeof(X), sr = a.r ? sizeof(Y) : 0;
     const NormBlockPlan p = norm_block_plan(a.rows, a.width, a.width * (sx + sr), false);
     const int64_t n = p.rows * static_cast<int64_t>(a.width);
