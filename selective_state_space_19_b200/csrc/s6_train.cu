@@ -389,7 +389,7 @@ int check_conv_bwd_dims(const s6_dims *dims) {
 // --------------------------------------------------------------- gradients
 constexpr int64_t kGradMaxNumel = int64_t(1) << 37;  // 2^26 of the smallest chunks
 
-int64_t grad_quads(int64_t numel, int32_t dtype) {  // of 4 bytes
+int64_t grad_words(int64_t numel, int32_t dtype) {  // float32 elements, or pairs of bfloat16 ones
     return dtype == S6_BF16 ? ceil_div(numel, 2) : numel;
 }
 
@@ -399,7 +399,7 @@ int64_t grad_quads(int64_t numel, int32_t dtype) {  // of 4 bytes
 int grad_chunk(int64_t count, const int64_t *numel, const int32_t *dtypes) {
     int64_t total = 0;
     for (int64_t i = 0; i < count; ++i)
-        total += grad_quads(numel[i], dtypes[i]);
+        total += grad_words(numel[i], dtypes[i]);
     const int64_t blocks = s6::kGradMaxBlocks, rounds = std::max<int64_t>(1, ceil_div(total, blocks * s6::kGradChunkMost));
     const int64_t chunks = std::max(blocks * rounds - count, blocks * rounds / 2);
     const int64_t chunk = ceil_div(ceil_div(total, chunks), s6::kGradChunkStep) * s6::kGradChunkStep;
@@ -455,7 +455,7 @@ int for_tables(int64_t count, const void *const *grads, const int64_t *numel, co
     for (int64_t i = 0; i < count; ++i) {
         if (numel[i] == 0)
             continue;
-        const int chunks = static_cast<int>(ceil_div(grad_quads(numel[i], dtypes[i]), t.chunk));  // at most 2^26 (check_grads)
+        const int chunks = static_cast<int>(ceil_div(grad_words(numel[i], dtypes[i]), t.chunk));  // at most 2^26 (check_grads)
         if (t.tensors == M || t.chunks + chunks > (1 << 30)) {
             const int rc = fn(t);
             if (rc != S6_OK)
