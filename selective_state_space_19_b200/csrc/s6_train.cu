@@ -206,13 +206,14 @@ auto norm_block_kernel(const s6::NormBwdBlockArgs &) {
     return s6::s6_layernorm_bwd_block_kernel<X, Y, V, NQ, R, T, norm_block_bound(T, NQ, true)>;
 }
 
-// Launches with more dynamic shared memory than the default 48 KB (the attribute
-// is the device's own; setting it costs little).
+// The default limit of 48 KB counts a block's static shared memory too.  Above it a
+// kernel's own limit is raised, always to the same value: the limit belongs to the
+// kernel on the device, and another thread's call may be between here and its launch.
 template <typename X, typename Y, int V, int NQ, int R, int T, typename Args>
 int norm_block_launch(const Args &a, const NormBlockPlan &p, int smem, cudaStream_t st) {
     auto kern = norm_block_kernel<X, Y, V, NQ, R, T>(a);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (smem > 48 * 1024 - kSmemBlock && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                              kSmemSM - kSmemBlock) != cudaSuccess)
         return S6_ERR_CUDA;
     kern<<<static_cast<unsigned>(p.blocks), T, static_cast<size_t>(smem), st>>>(a);
     return launch_status(cudaGetLastError());
