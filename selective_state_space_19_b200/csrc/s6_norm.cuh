@@ -9,6 +9,18 @@
 //     m = sum(s) / W,   q = 1 / sqrt(sum((s - m)^2) / W + eps)
 //     y = (s - m) q w + b
 //
+// A float32 sum times a rounded 1/W leaves m off by a few roundings of |m|: nothing
+// where |m| is at most the deviations' root mean square, but a row of the constant
+// 100 came out up to 5e-3 off by it, and rows at 1000 +- 0.01 up to 2e-2.  Where m is
+// larger ("far"), the deviations d from that first m are summed up too, and what m
+// was off by, c = sum(d) / W, is taken out:
+//
+//     sum((s - m)^2) / W = sum(d^2) / W - c^2,   y = (d - c) q w + b,   m = first m + c
+//
+// Far rows pay for a third reduction; in every row it cost 2 % on average and 5 to
+// 20 % of narrow and bfloat16 ones.  (The backward's h goes by the m that was stored,
+// a float32: of rows at 1000 +- 0.01 it is off by up to 3e-3.)
+//
 //     h = (s - m) q,    g = w dy
 //     dx = ds + q (g - sum(g)/W - h sum(g h)/W)        ds: the gradient that
 //     dw = sum over rows of dy h,  db = of dy          reaches s past the norm
@@ -97,6 +109,16 @@ __device__ __forceinline__ void quad_params(const float *p, float def, int c, in
     q[1] = f2_pack(f[2], f[3]);
 }
 
+// Whether a row's mean is large next to its deviations; sq: the mean of their squares.
+__device__ __forceinline__ bool norm_far(float mean, float sq) { return mean * mean > sq; }
+
+// The mean of the squares where the mean is taken `off` further on.  NaN stays NaN, and
+// squares that overflowed stay infinite (for a rstd of 0).
+__device__ __forceinline__ float norm_moved(float sq, float off) {
+    const float var = fmaf(-off, off, sq);
+    return var < 0.0f ? 0.0f : var;
+}
+
 constexpr int kNormWideThreads = 512;
 
 // The sum of v over a block of kNormWideThreads, through `red` (one slot a warp).
@@ -165,8 +187,7 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         if (row + step < a.rows)
             fetch(row + step);
         const float mean = group_sum<G>(f2_sum(t0, t1)) * a.inv_w;
-        // squares of the deviations from the mean, not of the values: a mean that is
-        // large next to the deviations costs no digits
+        // squares of the deviations from the mean, not of the values
         t0 = t1 = f2_both(0.0f);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
@@ -177,31 +198,42 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
             t0 = f2_fma(v[j][0], v[j][0], t0);
             t1 = f2_fma(v[j][1], v[j][1], t1);
         }
-        const float rstd = __frsqrt_rn(group_sum<G>(f2_sum(t0, t1)) * a.inv_w + a.eps);
+        float sq = group_sum<G>(f2_sum(t0, t1)) * a.inv_w, off = 0.0f;
+        if (norm_far(mean, sq)) {  // the same for all lanes of a row
+            t0 = t1 = f2_both(0.0f);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                t0 = f2_add(t0, v[j][0]);
+                t1 = f2_add(t1, v[j][1]);
+            }
+            off = group_sum<G>(f2_sum(t0, t1)) * a.inv_w;
+            sq = norm_moved(sq, off);
+        }
+        const float rstd = __frsqrt_rn(sq + a.eps);
         if (lane == 0) {
             if (a.mean)
-                a.mean[row] = mean;
+                a.mean[row] = mean + off;
             if (a.rstd)
                 a.rstd[row] = rstd;
         }
-        const f2_t q = f2_both(rstd);
+        const f2_t q = f2_both(rstd), c = f2_both(-off * rstd);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const f2_t o[2] = {f2_fma(f2_mul(v[j][0], q), wv[j][0], bv[j][0]),
-                               f2_fma(f2_mul(v[j][1], q), wv[j][1], bv[j][1])};
+            const f2_t o[2] = {f2_fma(f2_fma(v[j][0], q, c), wv[j][0], bv[j][0]),
+                               f2_fma(f2_fma(v[j][1], q, c), wv[j][1], bv[j][1])};
             QY::store(y + row * W, j + 1 < NQ, col(j), G, W, o);
         }
     }
 }
 
 // Rows above kNormMaxWidth: a block walks its row three times
-// (sum, squared deviations, output); the second and third reads hit L2.  s is
+// (sum, deviations and their squares, output); the second and third reads hit L2.  s is
 // written on the last walk, since it may be x itself.
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel(const NormFwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
-    __shared__ float red[2][kNormWideThreads / 32];
+    __shared__ float red[3][kNormWideThreads / 32];
     const int W = a.width;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X *x = static_cast<const X *>(a.x) + row * W;
@@ -216,7 +248,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
                     v[i] += t[i];
             }
         };
-        float sum = 0.0f, sq = 0.0f;
+        float sum = 0.0f, sq = 0.0f, off = 0.0f;
         for (int c = threadIdx.x * V; c < W; c += kNormWideThreads * V) {
             float v[V];
             value(c, v);
@@ -229,13 +261,18 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
             float v[V];
             value(c, v);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
                 sq = fmaf(v[i] - mean, v[i] - mean, sq);
+                off += v[i] - mean;
+            }
         }
-        const float rstd = __frsqrt_rn(wide_sum(sq, red[1]) * a.inv_w + a.eps);
+        // bound by the walks: every row is treated as far
+        sq = wide_sum(sq, red[1]) * a.inv_w;
+        off = wide_sum(off, red[2]) * a.inv_w;
+        const float rstd = __frsqrt_rn(norm_moved(sq, off) + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean)
-                a.mean[row] = mean;
+                a.mean[row] = mean + off;
             if (a.rstd)
                 a.rstd[row] = rstd;
         }
@@ -246,7 +283,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
                 VX::store(static_cast<X *>(a.s) + row * W + c, VX::pack(v));
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                o[i] = fmaf((v[i] - mean) * rstd, a.w ? a.w[c + i] : 1.0f, a.b ? a.b[c + i] : 0.0f);
+                o[i] = fmaf(((v[i] - mean) - off) * rstd, a.w ? a.w[c + i] : 1.0f, a.b ? a.b[c + i] : 0.0f);
             VY::store(static_cast<Y *>(a.y) + row * W + c, VY::pack(o));
         }
     }
@@ -448,11 +485,15 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
     const NormFwdArgs &a = args.n;
     extern __shared__ __align__(16) unsigned char s6_norm_smem[];
     __shared__ uint64_t full[kNormMaxStages];
-    __shared__ float slots[2][4][16];
+    __shared__ float slots[3][4][16];
     const int tid = threadIdx.x, W = a.width;
     const X *x = static_cast<const X *>(a.x);
     const Y *r = static_cast<const Y *>(a.r);
     auto col = [&](int j) { return tid * V + 4 * T * j; };  // only the last quad can pass the row's end
+    // Three quads a thread are summed up behind their loads, which takes 80 registers (between
+    // them 82 in one form: a block fewer on an SM, 8191x2561 f32 to bfloat16 37 us for 27); four
+    // between their loads, 93 for 121 (16384x2047 bfloat16 33 us for 45).
+    constexpr bool kSumsBehind = NQ == 3;
     const long long steps = (a.rows + R - 1) / R, total = a.rows * W;
     NormRing ring{s6_norm_smem, full, args.s.stages, args.s.x_bytes + args.s.y_bytes, 0, 0u};
 
@@ -513,8 +554,17 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
                     if (a.s)
                         QX::store(static_cast<X *>(a.s) + (row + k) * W, j + 1 < NQ, col(j), T, W, v[k][j]);
                 }
-                t0 = f2_add(t0, v[k][j][0]);
-                t1 = f2_add(t1, v[k][j][1]);
+                if constexpr (!kSumsBehind) {
+                    t0 = f2_add(t0, v[k][j][0]);
+                    t1 = f2_add(t1, v[k][j][1]);
+                }
+            }
+            if constexpr (kSumsBehind) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    t0 = f2_add(t0, v[k][j][0]);
+                    t1 = f2_add(t1, v[k][j][1]);
+                }
             }
             sum[k] = f2_sum(t0, t1);
         }
@@ -529,15 +579,15 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
         if (tid == 0 && step + static_cast<long long>(ring.stages) * gridDim.x < steps)
             fetch(ring.st, step + static_cast<long long>(ring.stages) * gridDim.x);
         ring.next();
-        float mean[R], sq[R];
+        float sq[R], off[R];  // sum: the means from here on
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            mean[k] = sum[k] * a.inv_w;
+            sum[k] *= a.inv_w;
             f2_t t0 = f2_both(0.0f), t1 = t0;
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
                 f2_t m[2];
-                quad_where<V>(-mean[k], j + 1 < NQ, col(j), T, W, m);
+                quad_where<V>(-sum[k], j + 1 < NQ, col(j), T, W, m);
                 v[k][j][0] = f2_add(v[k][j][0], m[0]);
                 v[k][j][1] = f2_add(v[k][j][1], m[1]);
                 t0 = f2_fma(v[k][j][0], v[k][j][0], t0);
@@ -546,21 +596,48 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_fwd_block_kernel(const N
             sq[k] = f2_sum(t0, t1);
         }
         block_sums<R, WARPS>(sq, slots[1], false);
+        bool far = false;  // the same for all threads
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            sq[k] *= a.inv_w;
+            off[k] = 0.0f;
+            far = far || norm_far(sum[k], sq[k]);
+            if (tid == 0 && a.mean && k < here)
+                a.mean[row + k] = sum[k];
+        }
+        if (far) {
+            float dev[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                f2_t t0 = f2_both(0.0f), t1 = t0;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    t0 = f2_add(t0, v[k][j][0]);
+                    t1 = f2_add(t1, v[k][j][1]);
+                }
+                dev[k] = f2_sum(t0, t1);
+            }
+            block_sums<R, WARPS>(dev, slots[2], false);
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (norm_far(sum[k], sq[k])) {  // each row by itself, whatever shares its step
+                    off[k] = dev[k] * a.inv_w;
+                    sq[k] = norm_moved(sq[k], off[k]);
+                    if (tid == 0 && a.mean && k < here)
+                        a.mean[row + k] = sum[k] + off[k];
+                }
+        }
 #pragma unroll
         for (int k = 0; k < R; ++k)
             if (k < here) {
-                const float rstd = __frsqrt_rn(sq[k] * a.inv_w + a.eps);
-                if (tid == 0) {
-                    if (a.mean)
-                        a.mean[row + k] = mean[k];
-                    if (a.rstd)
-                        a.rstd[row + k] = rstd;
-                }
-                const f2_t q = f2_both(rstd);
+                const float rstd = __frsqrt_rn(sq[k] + a.eps);
+                if (tid == 0 && a.rstd)
+                    a.rstd[row + k] = rstd;
+                const f2_t q = f2_both(rstd), c = f2_both(-off[k] * rstd);
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const f2_t o[2] = {f2_fma(f2_mul(v[k][j][0], q), wv[j][0], bv[j][0]),
-                                       f2_fma(f2_mul(v[k][j][1], q), wv[j][1], bv[j][1])};
+                    const f2_t o[2] = {f2_fma(f2_fma(v[k][j][0], q, c), wv[j][0], bv[j][0]),
+                                       f2_fma(f2_fma(v[k][j][1], q, c), wv[j][1], bv[j][1])};
                     QY::store(static_cast<Y *>(a.y) + (row + k) * W, j + 1 < NQ, col(j), T, W, o);
                 }
             }

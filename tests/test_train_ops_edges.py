@@ -74,3 +74,66 @@ def test_layernorm_from_two_threads_with_different_sizes():
         # of ones: y is 0, a mean off by 2 u times rstd; dx is 1 - 1 - 1, each mean off by 2 u
         assert y.abs().max().item() <= 3 * R.U * 1e-5 ** -0.5, W
         assert (dx - (0.0 if W == 2560 else -1.0)).abs().max().item() <= 8 * R.U, W
+
+
+# ------------------------------------------------------- rows far from zero
+def _far_bounds(s, w, b, eps):
+    """Forward of rows s (float64 of what the kernel adds up) and what it may be off by: the
+    first mean by e1 = U (DEPTH + 2) mean|s|; then the deviations d, |d| <= |s - mean| + e1, by
+    a rounding each, and their own mean, which is taken out, by U (DEPTH + 2) of mean|d|."""
+    mean = s.mean(-1, keepdims=True)
+    dev = s - mean
+    var = (dev ** 2).mean(-1, keepdims=True)
+    rstd = 1.0 / np.sqrt(var + eps)
+    e1 = R.U * (R.DEPTH + 2) * np.abs(s).mean(-1, keepdims=True)
+    d = np.abs(dev) + e1
+    e_mean = R.U * (R.DEPTH + 3) * d.mean(-1, keepdims=True)
+    e_d = 2 * R.U * d + e_mean
+    e_var = R.U * (R.DEPTH + 6) * (d ** 2).mean(-1, keepdims=True) + (2 * np.abs(dev) * e_d + e_d ** 2).mean(-1, keepdims=True)
+    e_rstd = rstd * (0.5 * e_var / (var + eps) + 3 * R.U)
+    h = dev * rstd
+    y = h * w + b
+    e_y = np.abs(w) * (e_d * rstd + np.abs(dev) * e_rstd + 2 * R.U * np.abs(h)) + 2 * R.U * (np.abs(y) + np.abs(h * w))
+    return (y, mean[:, 0], rstd[:, 0]), (e_y, e_mean[:, 0] + R.U * np.abs(mean[:, 0]), e_rstd[:, 0])
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("W", [5, 40, 63, 64, 100, 130, 300, 384, 500, 771, 1000, 1535, 2561, 3001, 4100, 8191, 8192,
+                               9000, 20000])
+def test_layernorm_of_rows_far_from_zero(W, add):
+    """Constant rows, and rows whose mean is up to 1e5 times their deviations, by turns with
+    rows around zero: each within its bound, and the latter with the bits they have alone."""
+    import torch
+    import selective_state_space_19_b200 as S
+    rng = np.random.default_rng(W)
+    centre = np.array([0.0, 100.0, 0.1, 1e4, 1000.0, 0.0, 1000.0, 1e-3, 0.0, 77.7, 123.4, 0.0])[:, None]
+    dev = np.array([1.0, 0.0, 1.0, 0.0, 1.0, 1.0, 0.01, 1.0, 1.0, 0.0, 0.0, 1.0])[:, None]
+    x = (centre + dev * rng.standard_normal((12, W))).astype(np.float32)
+    r = (0.01 * dev * rng.standard_normal((12, W))).astype(np.float32)
+    w, b = rng.standard_normal(W).astype(np.float32), rng.standard_normal(W).astype(np.float32)
+    s = (x + r) if add else x  # the float32 sum
+    (y, mean, rstd), (e_y, e_mean, e_rstd) = _far_bounds(s.astype(np.float64), w, b, 1e-5)
+    assert e_y[[1, 3, 4, 6]].max() < 1e-3  # the bound itself keeps the digits
+    xd, rd, wd, bd = (to_dev(a) for a in (x, r, w, b))
+    got, _, m, q = S.s6_layernorm_fwd(xd, wd, bd, r=rd if add else None)
+    R.within(got.cpu().numpy(), y, e_y, "y")
+    R.within(m.cpu().numpy(), mean, e_mean, "mean")
+    R.within(q.cpu().numpy(), rstd, e_rstd, "rstd")
+    near = torch.tensor([0, 2, 5, 7, 8, 11], device="cuda")
+    alone = S.s6_layernorm_fwd(xd[near].contiguous(), wd, bd, r=rd[near].contiguous() if add else None)
+    assert torch.equal(alone[0], got[near]) and torch.equal(alone[2], m[near]) and torch.equal(alone[3], q[near])
+
+
+@pytest.mark.parametrize("W", [40, 300, 1001, 2560, 9000])
+def test_layernorm_of_bfloat16_rows_far_from_zero(W):
+    import torch
+    import selective_state_space_19_b200 as S
+    rng = np.random.default_rng(W)
+    x = torch.from_numpy((100.0 + np.array([[0.0], [0.5], [8.0]]) * rng.standard_normal((3, W))).astype(np.float32))
+    for xt in (torch.bfloat16, torch.float32):
+        s = x.bfloat16().to(xt)
+        (y, mean, rstd), (e_y, e_mean, e_rstd) = _far_bounds(s.double().numpy(), 1.0, 0.0, 1e-5)
+        got, _, m, q = S.s6_layernorm_fwd(s.cuda(), y_dtype=torch.bfloat16)
+        R.within(got.double().cpu().numpy(), y, e_y + R.HALF["bf16"] * (np.abs(y) + e_y), "y")
+        R.within(m.cpu().numpy(), mean, e_mean, "mean")
+        R.within(q.cpu().numpy(), rstd, e_rstd, "rstd")
