@@ -329,16 +329,19 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
         fetch(row);
     for (; row < a.rows; row += step) {
         f2_t h[NQ][2], g[NQ][2], s0 = f2_both(0.0f), s1 = s0;
-        const f2_t m = f2_both(-mean), q = f2_both(rstd);
+        const f2_t q = f2_both(rstd);
         const float rq = rstd;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
+            f2_t m[2];
             xr[j].pairs(h[j]);
             gr[j].pairs(g[j]);
+            // elements behind the row have g = 0 and h = 0 (not 0 - mean, which times rstd may
+            // be infinite) and add nothing
+            quad_where<V>(-mean, j + 1 < NQ, col(j), G, W, m);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                // elements behind the row have g = 0 and add nothing
-                h[j][i] = f2_mul(f2_add(h[j][i], m), q);
+                h[j][i] = f2_mul(f2_add(h[j][i], m[i]), q);
                 dw[j][i] = f2_fma(g[j][i], h[j][i], dw[j][i]);
                 db[j][i] = f2_add(db[j][i], g[j][i]);
                 g[j][i] = f2_mul(g[j][i], wv[j][i]);
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
                                                           in16(a.ds, row * W));
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const f2_t m = f2_both(-mean[k]), q2 = f2_both(rstd[k]);
+            const f2_t q2 = f2_both(rstd[k]);
             q[k] = rstd[k];
             f2_t s0 = f2_both(0.0f), s1 = s0;
 #pragma unroll
@@ -736,12 +739,15 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
                     xq.clear();
                     gq.clear();
                 }
+                f2_t m[2];
                 xq.pairs(h[k][j]);
                 gq.pairs(g[k][j]);
+                // what is behind the row, or a row that is not there, has g = 0 and h = 0 (not
+                // 0 - mean, which times rstd may be infinite) and adds nothing
+                quad_where<V>(-mean[k], j + 1 < NQ, col(j), T, W, m);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // what is behind the row, or a row that is not there, has g = 0 and adds nothing
-                    h[k][j][i] = f2_mul(f2_add(h[k][j][i], m), q2);
+                    h[k][j][i] = f2_mul(f2_add(h[k][j][i], m[i]), q2);
                     dw[j][i] = f2_fma(g[k][j][i], h[k][j][i], dw[j][i]);
                     db[j][i] = f2_add(db[j][i], g[k][j][i]);
                     g[k][j][i] = f2_mul(g[k][j][i], wv[j][i]);

@@ -137,3 +137,24 @@ def test_layernorm_of_bfloat16_rows_far_from_zero(W):
         R.within(got.double().cpu().numpy(), y, e_y + R.HALF["bf16"] * (np.abs(y) + e_y), "y")
         R.within(m.cpu().numpy(), mean, e_mean, "mean")
         R.within(q.cpu().numpy(), rstd, e_rstd, "rstd")
+
+
+@pytest.mark.parametrize("W", [5, 31, 33, 64, 65, 130, 383, 385, 516, 771, 1001, 2561, 4097, 8191, 9001])
+@pytest.mark.parametrize("xt,yt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+def test_layernorm_backward_of_rows_whose_mean_over_the_deviation_overflows(W, xt, yt):
+    """Columns behind a row's end take no part, however large the row's mean times its rstd
+    is (6e38 here, beside deviations of zero)."""
+    import torch
+    import selective_state_space_19_b200 as S
+    rng = np.random.default_rng(W)
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    x = torch.from_numpy(rng.standard_normal((5, W)).astype(np.float32)).to(types[xt])
+    x[1], x[4] = 2.0 ** 120, -2.0 ** 120
+    dy = torch.from_numpy(rng.standard_normal((5, W)).astype(np.float32)).to(types[yt])
+    w = rng.standard_normal(W).astype(np.float32)
+    mean, rstd = np.zeros(5, np.float32), np.ones(5, np.float32)
+    mean[[1, 4]], rstd[[1, 4]] = [2.0 ** 120, -2.0 ** 120], 1e-5 ** -0.5
+    ref, tol = R.ln_bwd(dy.double().numpy(), x.double().numpy(), mean.astype(np.float64), rstd.astype(np.float64), w)
+    got = S.s6_layernorm_bwd(dy.cuda(), x.cuda(), to_dev(mean), to_dev(rstd), to_dev(w))
+    for k in ("dx", "dw", "db"):
+        R.within(got[k].cpu().numpy(), ref[k], tol[k], k)
