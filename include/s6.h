@@ -540,7 +540,8 @@ S6_API int causal_conv1d_silu_bwd(const s6_dims *dims, const void *x, const floa
  *           many device pointers, element counts (up to 2^37; 0 allowed) and
  *           s6_dtypes, read during the call.  Tensors that are scaled must not
  *           overlap (S6_ERR_INVALID_ARG).
- *  norm     [1] f32 on the device: written (s6_grad_clip: read)
+ *  norm     [1] f32 on the device: written (s6_grad_clip: read).  Not inside a
+ *           tensor that is scaled (S6_ERR_INVALID_ARG).
  *  max_norm finite, >= 0;  eps finite, >= 0
  *
  * The norm holds over float32's whole range: squares do not overflow or vanish

@@ -576,7 +576,8 @@ def s6_grad_norm(grads, norm=None, stream=None):
 
 def s6_grad_clip(grads, norm, max_norm, eps=1e-6, stream=None):
     """Scales the gradients in place by min(1, max_norm / (norm + eps)), for a norm that is
-    on the device already (one that ranks have combined, say).  No two tensors may overlap."""
+    on the device already (one that ranks have combined, say).  No two tensors may overlap,
+    nor norm lie inside one."""
     grads = _grad_list(grads)
     if stream is not None:
         with _on(stream, norm):
@@ -586,7 +587,8 @@ def s6_grad_clip(grads, norm, max_norm, eps=1e-6, stream=None):
 
 def s6_clip_grad_norm(grads, max_norm, eps=1e-6, norm=None, stream=None):
     """s6_grad_norm and s6_grad_clip in one call: scales the gradients in place by
-    min(1, max_norm / (norm + eps)) and returns norm, as it was before."""
+    min(1, max_norm / (norm + eps)) and returns norm, as it was before.  norm: where to put
+    it (not inside a gradient)."""
     grads = _grad_list(grads)
     if stream is not None:
         with _on(stream, next((g for g in grads if g is not None), norm)):

@@ -521,6 +521,13 @@ int grads_common(int64_t count, const void *const *grads, const int64_t *numel, 
         return S6_ERR_INVALID_ARG;
     if (!aligned_to(norm_in, 4) || !aligned_to(norm_out, 4))
         return S6_ERR_ALIGNMENT;
+    // a norm inside a gradient would be scaled with it while other blocks read it
+    const uintptr_t norm = reinterpret_cast<uintptr_t>(squares ? norm_out : norm_in);
+    for (int64_t i = 0; scale && i < count; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]);
+        if (norm < at + static_cast<size_t>(numel[i]) * io_size(dtypes[i]) && at < norm + sizeof(float) && numel[i] > 0)
+            return S6_ERR_INVALID_ARG;
+    }
     if (squares) {
         rc = check_workspace(workspace, workspace_bytes, s6_grad_workspace(count, numel));
         if (rc != S6_OK)

@@ -158,3 +158,23 @@ def test_layernorm_backward_of_rows_whose_mean_over_the_deviation_overflows(W, x
     got = S.s6_layernorm_bwd(dy.cuda(), x.cuda(), to_dev(mean), to_dev(rstd), to_dev(w))
     for k in ("dx", "dw", "db"):
         R.within(got[k].cpu().numpy(), ref[k], tol[k], k)
+
+
+# ----------------------------------------------------------------- gradients
+def test_a_norm_beside_the_gradients_it_scales():
+    """In one buffer, right before and behind a gradient; inside one it is refused."""
+    import torch
+    import selective_state_space_19_b200 as S
+    buf = torch.full((1002,), 2.0, device="cuda")
+    for at in (0, 1001):
+        buf[1:1001] = 2.0
+        norm = S.s6_clip_grad_norm([buf[1:1001]], 1.0, eps=0.0, norm=buf[at:at + 1])
+        want = 2.0 * 1000 ** 0.5
+        assert abs(norm.item() - want) <= R.NORM_REL * want
+        assert (buf[1:1001] * want / 2.0 - 1.0).abs().max().item() <= 2 * R.SCALED_REL
+    for at in (1, 500, 1000):
+        with pytest.raises(S.S6Error):
+            S.s6_clip_grad_norm([buf[1:1001]], 1.0, norm=buf[at:at + 1])
+        with pytest.raises(S.S6Error):
+            S.s6_grad_clip([buf[1:1001]], buf[at:at + 1], 1.0)
+    assert S.s6_grad_norm([buf[1:1001]], norm=buf[5:6]) is not None  # read only: allowed
