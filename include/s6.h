@@ -98,7 +98,8 @@ typedef enum {
     S6_ERR_ALIGNMENT = -3,   /* pointer or row not 16-byte aligned              */
     S6_ERR_CUDA = -4,        /* a CUDA runtime call or launch failed            */
     S6_ERR_TIMEOUT = -5,     /* a bounded device-side wait gave up              */
-    S6_ERR_SCRATCH_LIMIT = -6 /* fixed scratch too small (s6_conv_scan_fwd_noalloc) */
+    S6_ERR_SCRATCH_LIMIT = -6, /* fixed scratch too small (s6_conv_scan_fwd_noalloc) */
+    S6_ERR_HOST_MEMORY = -7  /* no host memory to check a list of gradients     */
 } s6_status;
 
 /*

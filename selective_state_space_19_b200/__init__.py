@@ -35,6 +35,7 @@ LIB_PATH = os.path.join(_HERE, "libs6_b200.so")
 S6_F32, S6_BF16 = 0, 1
 S6_OK, S6_ERR_INVALID_ARG, S6_ERR_UNSUPPORTED, S6_ERR_ALIGNMENT, S6_ERR_CUDA, S6_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 S6_ERR_SCRATCH_LIMIT = -6
+S6_ERR_HOST_MEMORY = -7
 S6_DECAY_LIVE, S6_DECAY_CONST = 0, 1
 CKPT_EVERY = 16  # tokens between the states a training forward keeps for the backward
 

@@ -936,6 +936,7 @@ const char *s6_status_string(int status) {
         case S6_ERR_TIMEOUT: return "S6_ERR_TIMEOUT: a bounded device-side wait gave up";
         case S6_ERR_SCRATCH_LIMIT:
             return "S6_ERR_SCRATCH_LIMIT: the problem needs more carry scratch than the fixed 4 MiB array holds";
+        case S6_ERR_HOST_MEMORY: return "S6_ERR_HOST_MEMORY: no host memory to check the list of gradients";
         default: return "S6: unknown status";
     }
 }

@@ -430,7 +430,7 @@ int check_grads(int64_t count, const void *const *grads, const int64_t *numel, c
     };
     Range *r = static_cast<Range *>(std::malloc(sizeof(Range) * static_cast<size_t>(count)));
     if (!r)
-        return S6_ERR_INVALID_ARG;
+        return S6_ERR_HOST_MEMORY;
     size_t n = 0;
     for (int64_t i = 0; i < count; ++i)
         if (numel[i] > 0) {

@@ -35,3 +35,27 @@ def test_a_norm_inside_a_gradient_is_refused(S):
     assert L.s6_grad_clip(*g, P(4100), 1.0, 1e-6, None) == S.S6_ERR_INVALID_ARG
     g = _grads((4098,), (3,), (1,))
     assert L.s6_grad_clip(*g, P(4096), 1.0, 1e-6, None) == S.S6_ERR_INVALID_ARG
+
+
+def test_a_list_too_long_for_the_hosts_memory_says_so(S):
+    """16.7 million tensors want 268 MB for the check that no two overlap: under a limit of the
+    address space the call returns a status of its own."""
+    import subprocess
+    import sys
+    code = """
+import ctypes, resource, sys
+import numpy as np
+L = ctypes.CDLL(sys.argv[1])
+n = 1 << 24
+ptrs = np.arange(1, n + 1, dtype=np.uint64) * 64
+numel, types = np.ones(n, np.int64), np.zeros(n, np.int32)
+L.s6_grad_clip.argtypes = [ctypes.c_int64] + [ctypes.c_void_p] * 4 + [ctypes.c_float] * 2 + [ctypes.c_void_p]
+L.s6_status_string.restype = ctypes.c_char_p
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (128 << 20), resource.RLIM_INFINITY))
+st = L.s6_grad_clip(n, ptrs.ctypes.data, numel.ctypes.data, types.ctypes.data, 16, -1.0, 1e-6, None)  # refused in any case
+assert st == int(sys.argv[2]), st
+assert L.s6_status_string(st).startswith(b"S6_ERR_HOST_MEMORY")
+"""
+    out = subprocess.run([sys.executable, "-c", code, S.LIB_PATH, str(S.S6_ERR_HOST_MEMORY)], capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-2000:]
