@@ -39,6 +39,13 @@ template <typename... A>
     throw Raised{};
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw Raised{};
+    return v != 0;
+}
+
 const char *type_name(at::ScalarType t) { return c10::toString(t); }
 
 std::string shape_name(at::IntArrayRef shape) {
@@ -176,6 +183,7 @@ PyObject *layernorm_fwd(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
         const double eps = PyFloat_AsDouble(a[3]);
         if (eps == -1.0 && PyErr_Occurred())
             throw Raised{};
+        const bool want_stats = truth(a[8]);
         PyObject *po_r = a[4], *po_s = a[5], *po_y = a[6];
         at::ScalarType branch = x.scalar_type();
         if (a[7] != Py_None) {
@@ -202,7 +210,7 @@ PyObject *layernorm_fwd(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
             y = address(new_y = empty(shape, branch, dev));
         if (po_r != Py_None && po_s == Py_None)
             s = address(new_s = empty(shape, x.scalar_type(), dev));
-        if (PyObject_IsTrue(a[8])) {
+        if (want_stats) {
             mean = empty(rows, at::kFloat, dev);
             rstd = empty(rows, at::kFloat, dev);
         }
@@ -224,6 +232,7 @@ PyObject *layernorm_fwd(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
 PyObject *layernorm_bwd(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
     return guarded(nargs, 8, [&]() -> PyObject * {
         const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x");
+        const bool want_params = truth(a[7]);
         const s6_norm_dims dims = norm_dims(x, dy.scalar_type(), 0.0, "dy");
         const at::Device dev = x.device();
         const at::IntArrayRef shape = x.sizes(), width = shape.slice(shape.size() - 1),
@@ -237,7 +246,7 @@ PyObject *layernorm_bwd(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
         at::Tensor new_dx, dw, db;
         void *dx = a[6] == Py_None ? address(new_dx = empty(shape, at::kFloat, dev))
                                    : pointer(a[6], "dx", at::kFloat, shape, dev);
-        if (PyObject_IsTrue(a[7])) {
+        if (want_params) {
             dw = empty(width, at::kFloat, dev);
             db = empty(width, at::kFloat, dev);
         }

@@ -178,3 +178,14 @@ def test_a_norm_beside_the_gradients_it_scales():
         with pytest.raises(S.S6Error):
             S.s6_grad_clip([buf[1:1001]], buf[at:at + 1], 1.0)
     assert S.s6_grad_norm([buf[1:1001]], norm=buf[5:6]) is not None  # read only: allowed
+
+
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    import torch
+    import selective_state_space_19_b200 as S
+    x, m, two = torch.randn(4, 64, device="cuda"), torch.zeros(4, device="cuda"), torch.ones(2, dtype=torch.bool)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        S.s6_layernorm_fwd(x, want_stats=two)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        S.s6_layernorm_bwd(x, x, m, m, want_params=two)
+    assert S.s6_layernorm_fwd(x, want_stats=two[:1])[2] is not None
