@@ -180,6 +180,7 @@ __device__ __forceinline__ void bulk_fetch(unsigned char *buf, uintptr_t a, uint
             *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
         for (uintptr_t p = hi > a ? hi : a; p < b; p += sizeof(T))
             *reinterpret_cast<T *>(buf + (p - base)) = *reinterpret_cast<const T *>(p);
+        fence_proxy_async_smem();  // these stores before a later step's copy into the same bytes
         if (hi == lo)
             return;
     }

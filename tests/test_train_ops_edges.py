@@ -189,3 +189,126 @@ def test_a_flag_without_a_truth_value_raises_its_own_error():
     with pytest.raises(RuntimeError, match="ambiguous"):
         S.s6_layernorm_bwd(x, x, m, m, want_params=two)
     assert S.s6_layernorm_fwd(x, want_stats=two[:1])[2] is not None
+
+
+# ------------------------------------------------ many steps of a block's ring
+def _off(a, dtype, by):
+    """A contiguous tensor of a's values, `by` elements into its memory and with canaries
+    around it, and a function that tells whether those are as they were."""
+    import torch
+    buf = torch.full((a.numel() + by + 40,), 7.0, dtype=dtype, device="cuda")
+    t = buf[by:by + a.numel()].view(a.shape)
+    t.copy_(a)
+    return t, lambda: bool((buf[:by] == 7).all()) and bool((buf[by + a.numel():] == 7).all())
+
+
+OFF = {"on": (8, 16, 24, 32), "off": (1, 3, 5, 7)}  # elements into the memory
+RING = [(20001, 516), (9001, 1031), (6001, 2560), (4001, 4097), (3001, 8191), (9001, 384), (30001, 100), (90001, 30),
+        (1500, 9001)]
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("xt,yt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,W", RING)
+@pytest.mark.parametrize("at", ["on", "off"])
+def test_layernorm_of_many_rows_on_and_off_16_byte_boundaries(at, rows, W, xt, yt, add):
+    """Blocks that take many steps (each stage of their shared memory several times), on
+    tensors that begin on or off a 16-byte boundary, every row against float64."""
+    import torch
+    import selective_state_space_19_b200 as S
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator(device="cuda").manual_seed(rows + W)
+
+    def normal(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen)
+    x, x_whole = _off(normal(rows, W), types[xt], OFF[at][0])
+    r, r_whole = _off(normal(rows, W), types[yt], OFF[at][1])
+    y, y_whole = _off(torch.zeros(rows, W, device="cuda"), types[yt], OFF[at][2])
+    s, s_whole = _off(torch.zeros(rows, W, device="cuda"), types[xt], OFF[at][3])
+    w, b = normal(W), normal(W)
+    out = S.s6_layernorm_fwd(x, w, b, r=r if add else None, s=s if add else None, y=y, y_dtype=types[yt])
+    sums = (x.float() + r.float()) if add else x.float()
+    half = R.HALF[yt]
+    step = max(1, 8_000_000 // W)
+    for at in range(0, rows, step):
+        part = slice(at, at + step)
+        (ry, rm, rq), (ey, em, eq) = _far_bounds_on_gpu(sums[part].double(), w.double(), b.double(), 1e-5)
+        _within(y[part], ry, ey + half * (ry.abs() + ey), "y")
+        _within(out[2][part], rm, em, "mean")
+        _within(out[3][part], rq, eq, "rstd")
+    assert not add or torch.equal(s, sums.to(types[xt]))
+    assert x_whole() and r_whole() and y_whole() and s_whole()
+
+
+def _far_bounds_on_gpu(s, w, b, eps):
+    """_far_bounds in torch."""
+    mean = s.mean(-1, keepdim=True)
+    dev = s - mean
+    var = dev.square().mean(-1, keepdim=True)
+    rstd = (var + eps).rsqrt()
+    d = dev.abs() + R.U * (R.DEPTH + 2) * s.abs().mean(-1, keepdim=True)
+    e_mean = R.U * (R.DEPTH + 3) * d.mean(-1, keepdim=True)
+    e_d = 2 * R.U * d + e_mean
+    e_var = R.U * (R.DEPTH + 6) * d.square().mean(-1, keepdim=True) + (2 * dev.abs() * e_d + e_d ** 2).mean(-1, keepdim=True)
+    e_rstd = rstd * (0.5 * e_var / (var + eps) + 3 * R.U)
+    h = dev * rstd
+    y = h * w + b
+    e_y = w.abs() * (e_d * rstd + dev.abs() * e_rstd + 2 * R.U * h.abs()) + 2 * R.U * (y.abs() + (h * w).abs())
+    return (y, mean[:, 0], rstd[:, 0]), (e_y, e_mean[:, 0] + R.U * mean[:, 0].abs(), e_rstd[:, 0])
+
+
+def _within(got, ref, tol, what):
+    share = ((got.double() - ref).abs() / (tol + 1e-37)).max().item()
+    assert share <= 1.0, (what, share)  # NaN fails too
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("xt,yt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,W", RING)
+@pytest.mark.parametrize("at", ["on", "off"])
+def test_layernorm_backward_of_many_rows_on_and_off_16_byte_boundaries(at, rows, W, xt, yt, add):
+    import torch
+    import selective_state_space_19_b200 as S
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator(device="cuda").manual_seed(rows * 3 + W)
+
+    def normal(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen)
+    x, x_whole = _off(normal(rows, W), types[xt], OFF[at][0])
+    dy, dy_whole = _off(0.5 + normal(rows, W), types[yt], OFF[at][2])
+    ds, ds_whole = _off(normal(rows, W), torch.float32, OFF[at][1])
+    dx, dx_whole = _off(torch.zeros(rows, W, device="cuda"), torch.float32, OFF[at][0])
+    w, mean, rstd = normal(W), 0.1 * normal(rows), 1.0 + 0.1 * normal(rows)
+    got = S.s6_layernorm_bwd(dy, x, mean, rstd, w, ds=ds if add else None, dx=dx)
+    sums = {k: torch.zeros(W, dtype=torch.float64, device="cuda") for k in ("dw", "db", "e_dw", "e_db")}
+    step = max(1, 8_000_000 // W)
+    for at in range(0, rows, step):
+        part = slice(at, at + step)
+        ref, tol, h, e_h = _bwd_bounds_on_gpu(dy[part].double(), x[part].double(), mean[part].double()[:, None],
+                                              rstd[part].double()[:, None], w.double(), ds[part].double() if add else None)
+        _within(dx[part], ref, tol, "dx")
+        g = dy[part].double()
+        sums["dw"] += (g * h).sum(0)
+        sums["db"] += g.sum(0)
+        sums["e_dw"] += R.U * R.DEPTH * (g * h).abs().sum(0) + (g.abs() * e_h).sum(0)
+        sums["e_db"] += R.U * R.DEPTH * g.abs().sum(0)
+    _within(got["dw"], sums["dw"], sums["e_dw"], "dw")
+    _within(got["db"], sums["db"], sums["e_db"], "db")
+    assert x_whole() and dy_whole() and ds_whole() and dx_whole()
+
+
+def _bwd_bounds_on_gpu(dy, x, mean, rstd, w, ds):
+    """train_reference.ln_bwd's dx in torch, and h with its bound."""
+    h = (x - mean) * rstd
+    g = dy * w
+    c0, c1 = g.mean(-1, keepdim=True), (g * h).mean(-1, keepdim=True)
+    dx = rstd * (g - c0 - h * c1)
+    e_h = R.U * ((x - mean).abs() * rstd + 2 * h.abs())
+    e_c0 = R.U * (R.DEPTH + 3) * g.abs().mean(-1, keepdim=True)
+    e_c1 = R.U * (R.DEPTH + 3) * (g * h).abs().mean(-1, keepdim=True) + (g.abs() * e_h).mean(-1, keepdim=True)
+    e_dx = rstd * (2 * R.U * g.abs() + e_c0 + h.abs() * e_c1 + c1.abs() * e_h
+                   + 3 * R.U * (g.abs() + c0.abs() + (h * c1).abs())) + R.U * dx.abs()
+    if ds is not None:
+        dx = dx + ds
+        e_dx = e_dx + R.U * dx.abs()
+    return dx, e_dx, h, e_h
