@@ -312,3 +312,54 @@ def _bwd_bounds_on_gpu(dy, x, mean, rstd, w, ds):
         dx = dx + ds
         e_dx = e_dx + R.U * dx.abs()
     return dx, e_dx, h, e_h
+
+
+# ------------------------------------------------------ the conv's long runs
+def _conv_against_float64(x, g, w, b, channels, depth, monkeypatch):
+    """All three gradients of some channels (each is a problem of its own) against float64."""
+    import selective_state_space_19_b200 as S
+    monkeypatch.setattr(R, "DEPTH", depth)
+    got = S.causal_conv1d_silu_bwd(x, w, g, conv_b=b)
+    pick = [a.index_select(-1, channels).double().cpu().numpy() for a in (x, g)]
+    ref, tol = R.conv_bwd(pick[0], w[channels].double().cpu().numpy(), b[channels].double().cpu().numpy(), pick[1])
+    R.within(got["dx"].index_select(-1, channels).cpu().numpy(), ref["dx"], tol["dx"], "dx")
+    for k in ("dconv_w", "dconv_b"):
+        R.within(got[k][channels].cpu().numpy(), ref[k], tol[k], k)
+
+
+CONV_TYPES = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
+
+
+def _conv_inputs(shape, K, xt, gt):
+    import torch
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape) + K)
+    x = (2.0 * torch.randn(shape, device="cuda", generator=gen)).to(types[xt])
+    g = (0.3 + torch.randn(shape, device="cuda", generator=gen)).to(types[gt])
+    w, b = (torch.randn(n, device="cuda", generator=gen) for n in ((shape[2], K), (shape[2],)))
+    return x, g, w, b
+
+
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("xt,gt", CONV_TYPES)
+@pytest.mark.parametrize("shape", [(16, 300, 1536), (16, 300, 1535), (3, 1021, 1090), (2, 333, 5119)])
+def test_conv_backward_of_runs_of_many_groups(shape, xt, gt, K, monkeypatch):
+    """Runs of 12 to 50 tokens and more: the groups of 8 that look at no token's place, between
+    the first and the last ones, in pairs of channels and in single ones."""
+    import torch
+    x, g, w, b = _conv_inputs(shape, K, xt, gt)
+    d = shape[2]
+    channels = torch.tensor([*range(66), *range(d // 2, d // 2 + 66), *range(d - 66, d)], device="cuda")
+    _conv_against_float64(x, g, w, b, channels, R.DEPTH, monkeypatch)
+
+
+@pytest.mark.parametrize("K,xt,gt", [(4, "f32", "f32"), (3, "bf16", "f32"), (2, "bf16", "bf16")])
+@pytest.mark.parametrize("shape", [(1, 30000, 5120), (16, 1500, 5120), (15, 2621, 2559)])
+def test_conv_backward_of_runs_up_to_their_longest(shape, xt, gt, K, monkeypatch):
+    """Sequences cut at 1024 tokens, warps that take several runs: sums of up to 1024 terms in
+    float32 and of the runs in float64."""
+    import torch
+    x, g, w, b = _conv_inputs(shape, K, xt, gt)
+    d = shape[2]
+    channels = torch.tensor([*range(20), *range(d // 2, d // 2 + 20), *range(d - 20, d)], device="cuda")
+    _conv_against_float64(x, g, w, b, channels, 1024 + R.DEPTH, monkeypatch)
