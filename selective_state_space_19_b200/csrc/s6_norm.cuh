@@ -465,9 +465,10 @@ struct NormRing {
         }
     }
     // After a wait that gave up: one thread waits, with the same bound, for the copies of
-    // the `left` steps behind the present one that have been started.
+    // the present step and of the `left` steps behind it that have been started.
     __device__ __forceinline__ void drain(int left) {
         raise_device_error(kErrTrainCopy);
+        wait();
         for (int k = 0; k < left; ++k) {
             next();
             wait();
