@@ -120,6 +120,7 @@ __device__ __forceinline__ float norm_moved(float sq, float off) {
 }
 
 constexpr int kNormWideThreads = 512;
+constexpr int kNormWideBlocks = 4;  // of them on an SM
 
 // The sum of v over a block of kNormWideThreads, through `red` (one slot a warp).
 // Every thread adds the slots in the same order.
@@ -133,6 +134,25 @@ __device__ __forceinline__ float wide_sum(float v, float *red) {
     for (int i = 0; i < kNormWideThreads / 32; ++i)
         v += red[i];
     return v;
+}
+
+// A block's walk over a row of W elements: f(c, a, b) adds columns c .. c + V - 1 to two sums.
+// A thread's float32 sums run over kNormWideRun vectors at most and are then added to
+// a0 and b0 (of 2^24 columns it has 8,192 vectors).  U of them are in flight: four, or
+// two of the backward's two vectors (four would spill).
+constexpr int kNormWideRun = 64;
+
+template <int V, int U, typename F>
+__device__ __forceinline__ void wide_walk(int W, F f, float &a0, float &b0) {
+    for (int c = threadIdx.x * V; c < W;) {
+        const int span = kNormWideRun * kNormWideThreads * V, stop = W - c < span ? W : c + span;
+        float a = 0.0f, b = 0.0f;
+#pragma unroll U
+        for (; c < stop; c += kNormWideThreads * V)
+            f(c, a, b);
+        a0 += a;
+        b0 += b;
+    }
 }
 
 template <typename X, typename Y, int V, int NQ, int G>
@@ -230,7 +250,8 @@ __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * 
 // (sum, deviations and their squares, output); the second and third reads hit L2.  s is
 // written on the last walk, since it may be x itself.
 template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel(const NormFwdArgs a) {
+__global__ void __launch_bounds__(kNormWideThreads, kNormWideBlocks)
+    s6_layernorm_fwd_wide_kernel(const NormFwdArgs a) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
     __shared__ float red[3][kNormWideThreads / 32];
@@ -248,16 +269,16 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
                     v[i] += t[i];
             }
         };
-        float sum = 0.0f, sq = 0.0f, off = 0.0f;
-        for (int c = threadIdx.x * V; c < W; c += kNormWideThreads * V) {
+        float sum = 0.0f, sq = 0.0f, off = 0.0f, none = 0.0f;
+        wide_walk<V, 4>(W, [&](int c, float &sum, float &) {
             float v[V];
             value(c, v);
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 sum += v[i];
-        }
+        }, sum, none);
         const float mean = wide_sum(sum, red[0]) * a.inv_w;
-        for (int c = threadIdx.x * V; c < W; c += kNormWideThreads * V) {
+        wide_walk<V, 4>(W, [&](int c, float &sq, float &off) {
             float v[V];
             value(c, v);
 #pragma unroll
@@ -265,7 +286,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
                 sq = fmaf(v[i] - mean, v[i] - mean, sq);
                 off += v[i] - mean;
             }
-        }
+        }, sq, off);
         // bound by the walks: every row is treated as far
         sq = wide_sum(sq, red[1]) * a.inv_w;
         off = wide_sum(off, red[2]) * a.inv_w;
@@ -292,7 +313,15 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_fwd_wide_kernel
 // ----------------------------------------------------------------- backward
 // A lane owns the same columns of every row it meets, so dw and db stay in its
 // registers until the last one; the block then writes one row of partial sums
-// and s6_sum_parts_kernel adds those up.
+// and s6_sum_parts_kernel adds those up in float64.  4,000 float32 additions of a
+// gradient of 0.1 are off by 4e-5 of their sum, 256 by 2e-6, so in every form there
+// are so many blocks that a thread adds up norm_run rows at most.  (Sums kept in
+// shared memory between runs, with no more blocks than are resident, took 3 to 12 %
+// more time, tall or not.)  Rows of up to 64 elements, of which there may be many,
+// run over 2,048; the _wide kernels over 1,024, since 16000x12000 bfloat16 took 578 us
+// in runs of 256 and 482 in the 327 that fill the SMs.
+constexpr int norm_run(int width) { return width <= 64 ? 2048 : width <= kNormMaxWidth ? 256 : 1024; }
+
 template <typename X, typename Y, int V, int NQ, int G>
 __global__ void __launch_bounds__(32 * kNormBlockWarps, norm_warps_resident(4 * NQ, true) / kNormBlockWarps)
     s6_layernorm_bwd_kernel(const NormBwdArgs a) {
@@ -830,8 +859,8 @@ __global__ void __launch_bounds__(T, MINB) s6_layernorm_bwd_block_kernel(const N
 
 // Wide rows: the two sums of every row first (a block a row), ...
 template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_kernel(const NormBwdArgs a,
-                                                                                    float2 *sums) {
+__global__ void __launch_bounds__(kNormWideThreads, kNormWideBlocks)
+    s6_layernorm_bwd_wide_sums_kernel(const NormBwdArgs a, float2 *sums) {
     using VX = IoVec<X, V>;
     using VY = IoVec<Y, V>;
     __shared__ float red[2][kNormWideThreads / 32];
@@ -841,7 +870,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_k
         const Y *dy = static_cast<const Y *>(a.dy) + row * W;
         const float mean = a.mean[row], rstd = a.rstd[row];
         float s0 = 0.0f, s1 = 0.0f;
-        for (int c = threadIdx.x * V; c < W; c += kNormWideThreads * V) {
+        wide_walk<V, V == 4 ? 2 : 4>(W, [&](int c, float &s0, float &s1) {
             float h[V], g[V];
             VX::unpack(VX::load(x + c), h);
             VY::unpack(VY::load(dy + c), g);
@@ -851,7 +880,7 @@ __global__ void __launch_bounds__(kNormWideThreads) s6_layernorm_bwd_wide_sums_k
                 s0 += t;
                 s1 = fmaf(t, (h[i] - mean) * rstd, s1);
             }
-        }
+        }, s0, s1);
         s0 = wide_sum(s0, red[0]);
         s1 = wide_sum(s1, red[1]);
         if (threadIdx.x == 0)

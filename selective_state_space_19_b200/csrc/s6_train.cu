@@ -96,6 +96,12 @@ struct NormWarpPlan {
 // (31 KB with 20).  Without the add more warps are faster throughout.
 constexpr int64_t kNormAddReads = 38 * 1024;
 
+// Backward: rounds of the resident blocks, such that none of the `sums` rows of sums that
+// one round keeps is over more than norm_run rows.
+int64_t norm_rounds(int64_t rows, int64_t width, int64_t sums) {
+    return ceil_div(rows, sums * s6::norm_run(static_cast<int>(width)));
+}
+
 NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd, int64_t read = 0) {
     NormWarpPlan p;
     p.elems = static_cast<int>(4 * ceil_div(width, 128));
@@ -107,6 +113,8 @@ NormWarpPlan norm_warp_plan(int64_t rows, int64_t width, bool bwd, int64_t read 
     if (read)
         warps = std::min(warps, std::max<int64_t>(s6::kNormBlockWarps, kNormAddReads / (read * warp_rows)));
     p.blocks = std::min(ceil_div(rows, s6::kNormBlockWarps * warp_rows), kSMs * warps / s6::kNormBlockWarps);
+    if (bwd)
+        p.blocks *= norm_rounds(rows, width, p.blocks * s6::kNormBlockWarps * warp_rows);
     return p;
 }
 
@@ -147,6 +155,8 @@ NormBlockPlan norm_block_plan(int64_t rows, int64_t width, int64_t row_bytes, bo
     p.rows = p.quads <= norm_two_rows_quads(bwd) && 4 * std::min(most, fits(2)) >= 3 * most ? 2 : 1;
     p.per_sm = std::min(most, std::max(1, fits(p.rows)));
     p.blocks = std::min(ceil_div(rows, p.rows), kSMs * p.per_sm);
+    if (bwd)
+        p.blocks *= norm_rounds(rows, width, p.blocks);
     return p;
 }
 
@@ -158,10 +168,12 @@ int norm_stages(s6::NormStream &s, const NormBlockPlan &p) {
 }
 
 // Runs of rows of the wide backward's second kernel: enough blocks to fill the
-// SMs at its 128-thread blocks, whatever the vector width.
+// SMs at its 128-thread blocks, whatever the vector width, times the rounds (up to the
+// grid's 65,535, which 60 million rows have).
 int64_t norm_wide_runs(int64_t rows, int64_t width) {
     const int64_t tiles = ceil_div(width, s6::kNormColThreads * 4);
-    return std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
+    const int64_t runs = std::min<int64_t>(rows, std::max<int64_t>(1, kSMs * 8 / tiles));
+    return std::min<int64_t>(runs * norm_rounds(rows, width, runs), 65535);
 }
 
 template <typename X, typename Y, int V, int NQ, int G>
@@ -244,7 +256,7 @@ int norm_block_rows(const Args &a, const NormBlockPlan &p, int smem, cudaStream_
 template <typename X, typename Y, int V>
 int norm_fwd_v(const s6::NormFwdArgs &a, cudaStream_t st) {
     if (a.width > s6::kNormMaxWidth) {
-        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * 4);
+        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * s6::kNormWideBlocks);
         s6::s6_layernorm_fwd_wide_kernel<X, Y, V>
             <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a);
         return launch_status(cudaGetLastError());
@@ -275,7 +287,7 @@ int norm_bwd_v(const s6::NormBwdArgs &in, void *workspace, float *dw, float *db,
         part = static_cast<float *>(workspace) + 2 * a.rows;
         parts = norm_wide_runs(a.rows, a.width);
         a.part = params ? part : nullptr;
-        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * 4);
+        const int64_t blocks = std::min<int64_t>(a.rows, kSMs * s6::kNormWideBlocks);
         s6::s6_layernorm_bwd_wide_sums_kernel<X, Y, V>
             <<<static_cast<unsigned>(blocks), s6::kNormWideThreads, 0, st>>>(a, sums);
         const dim3 grid(static_cast<unsigned>(ceil_div(a.width, s6::kNormColThreads * V)),

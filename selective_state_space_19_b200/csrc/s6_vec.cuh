@@ -269,7 +269,7 @@ __device__ __forceinline__ double warp_sum(double v) {
 // The gradients of parameters are sums over rows that many blocks share.  Each
 // block writes its sums, part[row][seg][c] (seg < segs, c < cols), and this
 // kernel adds them up in a fixed order, so results repeat bit for bit (atomics
-// would not).  Segment `seg` of column c goes to out0[c * segs0 + seg] for
+// would not): four rows in float32, and those in float64.  Segment `seg` of column c goes to out0[c * segs0 + seg] for
 // seg < segs0, and to out1[c] for seg = segs0; a null output is not wanted.
 // A block owns 32 columns; warp w adds rows w, w + 16, ... and the 16 sums
 // are added in order of w.  The partials of one call are a few MB at most and
@@ -283,30 +283,31 @@ struct SumPartsArgs {
 constexpr int kSumPartsWarps = 16;
 
 __global__ void __launch_bounds__(32 * kSumPartsWarps) s6_sum_parts_kernel(const SumPartsArgs a) {
-    __shared__ float sh[kSumPartsWarps][32];
+    __shared__ double sh[kSumPartsWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long n = static_cast<long long>(a.cols) * a.segs;
     const long long i = static_cast<long long>(blockIdx.x) * 32 + lane;
     cudaGridDependencySynchronize();
-    float s = 0.0f;
+    double s = 0.0;
     if (i < n) {
         const float *p = a.part + i;
         int r = warp;
         for (; r + 3 * kSumPartsWarps < a.rows; r += 4 * kSumPartsWarps) {
             const float v0 = p[r * n], v1 = p[(r + kSumPartsWarps) * n], v2 = p[(r + 2 * kSumPartsWarps) * n],
                         v3 = p[(r + 3 * kSumPartsWarps) * n];
-            s += (v0 + v1) + (v2 + v3);
+            s += static_cast<double>((v0 + v1) + (v2 + v3));
         }
         for (; r < a.rows; r += kSumPartsWarps)
-            s += p[r * n];
+            s += static_cast<double>(p[r * n]);
     }
     sh[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && i < n) {
-        float t = 0.0f;
+        double sum = 0.0;
 #pragma unroll
         for (int w = 0; w < kSumPartsWarps; ++w)
-            t += sh[w][lane];
+            sum += sh[w][lane];
+        const float t = static_cast<float>(sum);
         const int seg = static_cast<int>(i / a.cols), c = static_cast<int>(i - static_cast<long long>(seg) * a.cols);
         if (seg < a.segs0) {
             if (a.out0)

@@ -363,3 +363,50 @@ def test_conv_backward_of_runs_up_to_their_longest(shape, xt, gt, K, monkeypatch
     d = shape[2]
     channels = torch.tensor([*range(20), *range(d // 2, d // 2 + 20), *range(d - 20, d)], device="cuda")
     _conv_against_float64(x, g, w, b, channels, 1024 + R.DEPTH, monkeypatch)
+
+
+# --------------------------------------------------------------- long sums
+@pytest.mark.parametrize("rows,W,run", [(60_000_000, 30, 2048), (12_000_000, 100, 256), (4_700_000, 516, 256),
+                                        (1_600_000, 2560, 256), (500_000, 9004, 1024)])
+def test_layernorm_parameter_gradients_of_tall_inputs(rows, W, run):
+    """Some thousands of rows for each thread, all with the gradient 0.1, whose float32 sum
+    drifts: dw and db are within a depth of run + 64 additions of the exact rows * 0.1 (a run of
+    rows, then the lanes' and warps' sums, and float64 over the blocks)."""
+    import torch
+    import selective_state_space_19_b200 as S
+    free, _ = torch.cuda.mem_get_info()
+    if free < 14 * rows * W:
+        pytest.skip("needs %d GB of device memory" % (14 * rows * W >> 30))
+    x = torch.zeros(rows, W, device="cuda")
+    dy = torch.full((rows, W), 0.1, device="cuda")
+    mean, rstd = torch.full((rows,), -1.0, device="cuda"), torch.ones(rows, device="cuda")  # h = 1
+    got = S.s6_layernorm_bwd(dy, x, mean, rstd)
+    want = rows * float(np.float32(0.1))
+    for k in ("dw", "db"):
+        assert (got[k].double() - want).abs().max().item() <= (run + 64) * R.U * want, k
+
+
+@pytest.mark.parametrize("W", [1 << 20, (1 << 22) + 1, 1 << 24])
+def test_layernorm_of_the_widest_rows(W):
+    """Rows of up to 2^24 columns: sums of a thread's up to 8,192 vectors."""
+    import torch
+    import selective_state_space_19_b200 as S
+    gen = torch.Generator(device="cuda").manual_seed(W)
+    x = 3.0 + torch.randn(2, W, device="cuda", generator=gen)
+    dy = 0.1 + 0.01 * torch.randn(2, W, device="cuda", generator=gen)
+    xs, gs = x.double(), dy.double()
+    mean = xs.mean(-1, keepdim=True)
+    rstd = ((xs - mean).square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    h = (xs - mean) * rstd
+    y, _, m, q = S.s6_layernorm_fwd(x)
+    depth = 4 * 64 + 128 + 32  # a run's elements; the runs; the block's 5 + 16
+    # the mean is corrected by the deviations' own, so it is off by a few roundings of itself
+    assert ((m.double() - mean[:, 0]).abs() / (2 * R.U * mean[:, 0].abs() + depth * R.U)).max().item() <= 1.0
+    assert ((q.double() - rstd[:, 0]).abs() / rstd[:, 0]).max().item() <= depth * R.U
+    assert ((y.double() - h).abs() - 2 * depth * R.U * (1.0 + h.abs())).max().item() <= 0.0
+    mf, qf = mean[:, 0].float(), rstd[:, 0].float()
+    got = S.s6_layernorm_bwd(dy, x, mf, qf)
+    (ref, tol, _, _) = _bwd_bounds_on_gpu(gs, xs, mf.double()[:, None], qf.double()[:, None],
+                                          torch.ones(W, dtype=torch.float64, device="cuda"), None)
+    tol = tol * (depth + 3) / (R.DEPTH + 3)  # its means' sums are deeper
+    _within(got["dx"], ref, tol, "dx")
