@@ -455,6 +455,9 @@ S6_API int s6_block_step(const s6_block_dims *dims, const s6_block_weights *w, f
  * any streams, and may be captured into graphs without an earlier call.  All sums are made in a
  * fixed order: the same arguments give the same bits.  Pointers need only
  * element alignment (wider vectors are used where alignment and sizes allow).
+ * Outputs (and the workspace) that overlap one another or an input are refused
+ * with S6_ERR_INVALID_ARG, but where an argument below says that it may be the
+ * very same memory.
  * With a NULL or per-thread default stream the tensors must be on the calling
  * thread's current device.
  */
@@ -481,7 +484,7 @@ typedef struct {
  *  w, b  [width]      f32      NULL = ones, zeros
  *  s     [rows,width] x_dtype  written: x + r (may be x itself); NULL = not
  *                              wanted.  Must be NULL without r.
- *  y     [rows,width] y_dtype  written
+ *  y     [rows,width] y_dtype  written (may be x or r itself, where s is not)
  *  mean, rstd [rows]  f32      written, for the backward; NULL = not wanted
  *
  * m, rstd and y come from the float32 sum x + r, before its rounding to s.
@@ -502,8 +505,8 @@ S6_API int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void 
  *  dy         [rows,width] y_dtype  gradient with respect to y
  *  ds         [rows,width] f32      gradient that reaches the stream past the
  *                                   norm; NULL = zeros
- *  dx         [rows,width] f32      written (may be ds itself): with respect to
- *                                   s, and so to x and to r
+ *  dx         [rows,width] f32      written (may be ds itself, or a float32 x or
+ *                                   dy): with respect to s, and so to x and to r
  *  dw, db     [width]      f32      written; NULL = not wanted
  */
 S6_API int64_t s6_layernorm_bwd_workspace(const s6_norm_dims *dims);

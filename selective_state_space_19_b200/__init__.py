@@ -520,7 +520,8 @@ def s6_layernorm_fwd(x, w=None, b=None, eps=1e-5, r=None, s=None, y=None, y_dtyp
     """LayerNorm over the last dimension of the residual stream x [..., W], after adding
     a branch's output r (None: nothing to add).  w, b [W] float32 (None: ones, zeros).
     The branch type y_dtype (of r and y) is x's, or bfloat16 beside a float32 x; it
-    defaults to r's or y's, else to x's.  s: where to put x + r (x itself is allowed).
+    defaults to r's or y's, else to x's.  s: where to put x + r (x itself is allowed); y:
+    where to put the result.  Other overlaps of outputs are refused.
     Returns (y, s, mean, rstd): s is x when there is no r; mean and rstd [...] float32
     are for s6_layernorm_bwd (None unless want_stats)."""
     if stream is not None:
@@ -533,7 +534,7 @@ def s6_layernorm_bwd(dy, x, mean, rstd, w=None, ds=None, dx=None, want_params=Tr
     """Gradients of s6_layernorm_fwd: x is what was normalised (the forward's s), mean and
     rstd are its statistics, dy [..., W] is in the branch type; ds [..., W] float32 is the
     gradient that reaches the stream past the norm (None: zeros), and is added.  dx: where
-    to put the stream's gradient (ds itself is allowed).  Returns a dict of float32
+    to put the stream's gradient (ds itself is allowed, other overlaps are refused).  Returns a dict of float32
     tensors: dx [..., W] (with respect to s, and so to x and r), dw and db [W] (None
     unless want_params)."""
     if stream is not None:

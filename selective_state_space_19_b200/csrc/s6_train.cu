@@ -70,6 +70,35 @@ int check_workspace(const void *ws, int64_t bytes, int64_t need) {
     return ws && !aligned_to(ws, 8) ? S6_ERR_ALIGNMENT : S6_OK;
 }
 
+// The memory of an argument.  kEach: read element by element, so an output may be the
+// very same memory (as large, so of elements as large).
+enum Use { kRead, kEach, kWritten };
+struct Mem {
+    const void *p;
+    int64_t rows, row_bytes;
+    Use use;
+    uint64_t bytes() const {  // at most 2^66 by the checked sizes
+        uint64_t n;
+        return __builtin_mul_overflow(static_cast<uint64_t>(rows), static_cast<uint64_t>(row_bytes), &n) ? ~uint64_t(0) : n;
+    }
+};
+
+// Refuses outputs that share memory with one another or with an input.
+template <size_t N>
+int check_apart(const Mem (&m)[N]) {
+    for (size_t i = 0; i < N; ++i)
+        for (size_t j = 0; j < N; ++j) {
+            if (i == j || m[i].use != kWritten || !m[i].p || !m[j].p || (m[j].use == kWritten && j < i))
+                continue;
+            const uint64_t a = reinterpret_cast<uintptr_t>(m[i].p), b = reinterpret_cast<uintptr_t>(m[j].p);
+            const uint64_t an = m[i].bytes(), bn = m[j].bytes();
+            const bool overlap = an && bn && (a <= b ? b - a < an : a - b < bn);
+            if (overlap && !(m[j].use == kEach && a == b && an == bn))
+                return S6_ERR_INVALID_ARG;
+        }
+    return S6_OK;
+}
+
 // ---------------------------------------------------------------- LayerNorm
 int check_norm_dims(const s6_norm_dims *dims) {
     if (!dims || dims->rows < 0 || dims->width < 1 || !std::isfinite(dims->eps) || dims->eps < 0.0f)
@@ -580,6 +609,12 @@ int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void *r, con
     if (!aligned_to(x, sx) || !aligned_to(s, sx) || !aligned_to(r, sy) || !aligned_to(y, sy) || !aligned_to(w, 4) ||
         !aligned_to(b, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return S6_ERR_ALIGNMENT;
+    const int64_t rows = dims->rows, W = dims->width, xb = W * static_cast<int64_t>(sx), yb = W * static_cast<int64_t>(sy);
+    const Mem mem[] = {{s, rows, xb, kWritten}, {y, rows, yb, kWritten}, {mean, rows, 4, kWritten},
+                       {rstd, rows, 4, kWritten}, {x, rows, xb, kEach}, {r, rows, yb, kEach}, {w, 1, 4 * W, kRead},
+                       {b, 1, 4 * W, kRead}};
+    if (check_apart(mem) != S6_OK)
+        return S6_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (use_stream_device(st) != S6_OK)
         return S6_ERR_CUDA;
@@ -635,7 +670,15 @@ int s6_layernorm_bwd(const s6_norm_dims *dims, const void *x, const float *mean,
     if (!aligned_to(x, sx) || !aligned_to(dy, sy) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
         !aligned_to(w, 4) || !aligned_to(ds, 4) || !aligned_to(dx, 4) || !aligned_to(dw, 4) || !aligned_to(db, 4))
         return S6_ERR_ALIGNMENT;
-    rc = check_workspace(workspace, workspace_bytes, s6_layernorm_bwd_workspace(dims));
+    const int64_t rows = dims->rows, W = dims->width, xb = W * static_cast<int64_t>(sx), yb = W * static_cast<int64_t>(sy);
+    const int64_t need = s6_layernorm_bwd_workspace(dims);
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc != S6_OK)
+        return rc;
+    const Mem mem[] = {{dx, rows, 4 * W, kWritten}, {dw, 1, 4 * W, kWritten}, {db, 1, 4 * W, kWritten},
+                       {workspace, 1, need, kWritten}, {x, rows, xb, kEach}, {dy, rows, yb, kEach},
+                       {ds, rows, 4 * W, kEach}, {mean, rows, 4, kRead}, {rstd, rows, 4, kRead}, {w, 1, 4 * W, kRead}};
+    rc = check_apart(mem);
     if (rc != S6_OK)
         return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -698,7 +741,16 @@ int causal_conv1d_silu_bwd(const s6_dims *dims, const void *x, const float *conv
     if (!aligned_to(x, io_size(dims->io_dtype)) || !aligned_to(dout, io_size(dout_dtype)) || !aligned_to(dx, 4) ||
         !aligned_to(conv_w, 4) || !aligned_to(conv_b, 4) || !aligned_to(dconv_w, 4) || !aligned_to(dconv_b, 4))
         return S6_ERR_ALIGNMENT;
-    rc = check_workspace(workspace, workspace_bytes, causal_conv1d_silu_bwd_workspace(dims));
+    const int64_t need = causal_conv1d_silu_bwd_workspace(dims), tokens = Bt * L;
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc != S6_OK)
+        return rc;
+    // x and dout are read around a token, too: dx may be neither
+    const int64_t xb = d * static_cast<int64_t>(io_size(dims->io_dtype)), gb = d * static_cast<int64_t>(io_size(dout_dtype));
+    const Mem mem[] = {{dx, tokens, 4 * d, kWritten}, {dconv_w, K, 4 * d, kWritten}, {dconv_b, 1, 4 * d, kWritten},
+                       {workspace, 1, need, kWritten}, {x, tokens, xb, kRead}, {dout, tokens, gb, kRead},
+                       {conv_w, K, 4 * d, kRead}, {conv_b, 1, 4 * d, kRead}};
+    rc = check_apart(mem);
     if (rc != S6_OK)
         return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

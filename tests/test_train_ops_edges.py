@@ -410,3 +410,32 @@ def test_layernorm_of_the_widest_rows(W):
                                           torch.ones(W, dtype=torch.float64, device="cuda"), None)
     tol = tol * (depth + 3) / (R.DEPTH + 3)  # its means' sums are deeper
     _within(got["dx"], ref, tol, "dx")
+
+
+# ------------------------------------------------------------ shared memory
+@pytest.mark.parametrize("W", [40, 384, 1001, 2560, 9001])
+def test_outputs_in_the_place_of_their_inputs(W):
+    """y in x or r, dx in x, dy or ds: the same bits as apart; overlaps that are not element on
+    element are refused."""
+    import torch
+    import selective_state_space_19_b200 as S
+    x, r, ds = (torch.randn(700, W, device="cuda") for _ in range(3))
+    y, s, mean, rstd = S.s6_layernorm_fwd(x, r=r)
+    for into in (0, 1):
+        a = [x.clone(), r.clone()]
+        assert torch.equal(S.s6_layernorm_fwd(a[0], r=a[1], y=a[into])[0], y) and torch.equal(a[into], y)
+    a = [x.clone(), r.clone()]
+    y2, s2, _, _ = S.s6_layernorm_fwd(a[0], r=a[1], s=a[0], y=a[1])
+    assert torch.equal(y2, y) and torch.equal(s2, s)
+    dx = S.s6_layernorm_bwd(r, s, mean, rstd, ds=ds)["dx"]
+    for into in range(3):
+        a = [r.clone(), s.clone(), ds.clone()]
+        assert torch.equal(S.s6_layernorm_bwd(a[0], a[1], mean, rstd, ds=a[2], dx=a[into])["dx"], dx)
+    buf = torch.zeros(701 * W, device="cuda")
+    lo, hi = buf[:700 * W].view(700, W), buf[W:].view(700, W)
+    for call in (lambda: S.s6_layernorm_fwd(lo, y=hi), lambda: S.s6_layernorm_fwd(x, r=r, s=lo, y=lo),
+                 lambda: S.s6_layernorm_fwd(x, r=hi, s=lo), lambda: S.s6_layernorm_fwd(x, w=buf[5:5 + W], y=lo),
+                 lambda: S.s6_layernorm_bwd(x, lo, mean, rstd, dx=hi),
+                 lambda: S.s6_layernorm_bwd(x, s, buf[:700], rstd, dx=lo)):
+        with pytest.raises(S.S6Error):
+            call()

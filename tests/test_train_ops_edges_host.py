@@ -59,3 +59,60 @@ assert L.s6_status_string(st).startswith(b"S6_ERR_HOST_MEMORY")
 """
     out = subprocess.run([sys.executable, "-c", code, S.LIB_PATH, str(S.S6_ERR_HOST_MEMORY)], capture_output=True, text=True)
     assert out.returncode == 0, out.stderr[-2000:]
+
+
+BASE = 1 << 20
+
+
+def test_layernorm_forward_refuses_outputs_that_overlap(S):
+    """16 rows of 64 (4 KB in float32) at addresses a megabyte apart, but for the one that is moved."""
+    at = {k: BASE * (i + 1) for i, k in enumerate(("x", "r", "w", "b", "s", "y", "mean", "rstd"))}
+    size = dict(x=4096, r=4096, w=256, b=256, s=4096, y=4096, mean=64, rstd=64)
+    dims = S.NormDims(16, 64, S.S6_F32, S.S6_F32, 1e-5)
+
+    def status(**moved):
+        p = dict(at, **moved)
+        return S.lib().s6_layernorm_fwd(ctypes.byref(dims), P(p["x"]), P(p["r"]), P(p["w"]), P(p["b"]), P(p["s"]),
+                                        P(p["y"]), P(p["mean"]), P(p["rstd"]), None)
+    for out in ("s", "y", "mean", "rstd"):
+        for other in set(at) - {out}:
+            for by in (-size[out] + 4, size[other] - 4) + (() if other in "xr" and out in "sy" else (0,)):
+                assert status(**{out: at[other] + by}) == S.S6_ERR_INVALID_ARG, (out, other, by)
+    assert status(s=at["x"], y=at["x"]) == S.S6_ERR_INVALID_ARG  # both outputs in the stream
+    # rows and widths whose product passes 64 bits
+    dims = S.NormDims(1 << 40, 1 << 24, S.S6_F32, S.S6_F32, 1e-5)
+    assert status() == S.S6_ERR_INVALID_ARG
+
+
+def test_layernorm_backward_refuses_outputs_that_overlap(S):
+    names = ("x", "mean", "rstd", "w", "dy", "ds", "dx", "dw", "db", "ws")
+    at = {k: BASE * (i + 1) for i, k in enumerate(names)}
+    dims = S.NormDims(16, 64, S.S6_F32, S.S6_F32, 0.0)
+    ws = S.lib().s6_layernorm_bwd_workspace(ctypes.byref(dims))
+    size = dict(x=4096, mean=64, rstd=64, w=256, dy=4096, ds=4096, dx=4096, dw=256, db=256, ws=ws)
+
+    def status(**moved):
+        p = dict(at, **moved)
+        return S.lib().s6_layernorm_bwd(ctypes.byref(dims), *(P(p[k]) for k in names), ws, None)
+    for out in ("dx", "dw", "db", "ws"):
+        for other in set(at) - {out}:
+            for by in (-size[out] + 8, size[other] - 8) + (() if (out, other) in (("dx", "x"), ("dx", "dy"), ("dx", "ds")) else (0,)):
+                assert status(**{out: at[other] + by}) == S.S6_ERR_INVALID_ARG, (out, other, by)
+
+
+def test_conv_backward_refuses_outputs_that_overlap(S):
+    names = ("x", "w", "b", "g", "dx", "dw", "db", "ws")
+    at = {k: BASE * (i + 1) for i, k in enumerate(names)}
+    dims = S.Dims(2, 8, 64, 1, 4, 0)
+    ws = S.lib().causal_conv1d_silu_bwd_workspace(ctypes.byref(dims))
+    size = dict(x=4096, w=1024, b=256, g=4096, dx=4096, dw=1024, db=256, ws=ws)
+
+    def status(**moved):
+        p = {k: P(v) for k, v in dict(at, **moved).items()}
+        return S.lib().causal_conv1d_silu_bwd(ctypes.byref(dims), p["x"], p["w"], p["b"], p["g"], 0, p["dx"], p["dw"],
+                                              p["db"], p["ws"], ws, None)
+    assert ws < BASE
+    for out in ("dx", "dw", "db", "ws"):
+        for other in set(at) - {out}:
+            for by in (-size[out] + 8, 0, size[other] - 8):
+                assert status(**{out: at[other] + by}) == S.S6_ERR_INVALID_ARG, (out, other, by)
