@@ -116,3 +116,77 @@ def test_conv_backward_refuses_outputs_that_overlap(S):
         for other in set(at) - {out}:
             for by in (-size[out] + 8, 0, size[other] - 8):
                 assert status(**{out: at[other] + by}) == S.S6_ERR_INVALID_ARG, (out, other, by)
+
+
+# -------------------------------------------------------------------- build
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    """The build on a small source tree, with compilers that write down what they are asked for
+    (and fail on a source that holds the word broken)."""
+    from selective_state_space_19_b200 import _build
+    csrc = tmp_path / "csrc"
+    csrc.mkdir()
+    for name in ("a.cu", "s6_torch.cpp"):
+        (csrc / name).write_text("// " + name + "\n")
+    log = tmp_path / "log"
+    for name in ("nvcc", "cxx"):
+        tool = tmp_path / name
+        tool.write_text('#!/bin/sh\necho %s "$@" >> %s\nfor a; do case "$a" in *.cu|*.cpp) grep -q broken "$a" && exit 1;; esac; '
+                        '[ "$last" = -o ] && : > "$a"; last="$a"; done; exit 0\n' % (name, log))
+        tool.chmod(0o755)
+    for k, v in dict(HERE=str(tmp_path), CSRC=str(csrc), OBJ=str(csrc / "obj"), LIB=str(tmp_path / "lib.so"),
+                     MODULE=str(tmp_path / "_s6_torch.so"), CXX=str(tmp_path / "cxx")).items():
+        monkeypatch.setattr(_build, k, v)
+    monkeypatch.setattr(_build, "_nvcc", lambda: str(tmp_path / "nvcc"))
+
+    def calls():
+        lines = log.read_text().splitlines() if log.exists() else []
+        log.write_text("")
+        return sorted(l.split()[0] for l in lines)
+    return _build, tmp_path, calls
+
+
+def test_build_makes_both_and_then_nothing(tree):
+    B, at, calls = tree
+    B.build()
+    assert calls() == ["cxx", "cxx", "nvcc", "nvcc"] and (at / "lib.so").exists() and (at / "_s6_torch.so").exists()
+    assert B.up_to_date()
+    B.build()
+    assert calls() == []
+
+
+def test_build_without_torch_makes_the_library(tree, monkeypatch, capsys):
+    B, at, calls = tree
+    monkeypatch.setattr(B, "_torch_dir", lambda: None)
+    B.build()
+    assert calls() == ["nvcc", "nvcc"] and (at / "lib.so").exists() and not (at / "_s6_torch.so").exists()
+    assert "_s6_torch.so is not built" in capsys.readouterr().err
+    assert B.up_to_date()
+    monkeypatch.undo()
+
+
+def test_build_makes_the_library_where_the_module_cannot_be_made(tree, monkeypatch):
+    import subprocess
+    B, at, calls = tree
+    (at / "csrc" / "s6_torch.cpp").write_text("broken\n")
+    with pytest.raises(subprocess.CalledProcessError):
+        B.build()
+    assert (at / "lib.so").exists() and not (at / "_s6_torch.so").exists() and not B.up_to_date()
+    (at / "csrc" / "s6_torch.cpp").write_text("// mended\n")
+    monkeypatch.setattr(B, "CXX", str(at / "no such compiler"))
+    (at / "lib.so").unlink()
+    with pytest.raises(subprocess.CalledProcessError):
+        B.build()
+    assert (at / "lib.so").exists() and not (at / "_s6_torch.so").exists()
+
+
+def test_build_makes_the_module_again_for_another_torch(tree, monkeypatch):
+    B, at, calls = tree
+    B.build()
+    calls()
+    was = B._made_for()
+    monkeypatch.setattr(B, "_made_for", lambda: was + " and a half")
+    assert not B.up_to_date()
+    B.build()
+    assert calls() == ["cxx", "cxx", "nvcc"]  # the library is linked again, not compiled
+    assert B.up_to_date()
