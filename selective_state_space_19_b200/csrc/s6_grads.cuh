@@ -30,6 +30,8 @@
 // 66 tensors).  Four blocks an SM against six and eight: 486, 500, 497 us.
 #pragma once
 
+#include <cfloat>
+
 #include "s6_vec.cuh"
 
 namespace s6 {
@@ -151,7 +153,7 @@ __device__ __forceinline__ double chunk_square_sum(const T *p, int n) {
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(T *p, int n, float scale) {
+__device__ __forceinline__ void chunk_scale(T *p, int n, float scale, float post) {
     constexpr int V = GradChunk<T>::V;
     using Vec = IoVec<T, V>;
     const GradChunk<T> c(p, n);
@@ -162,12 +164,12 @@ __device__ __forceinline__ void chunk_scale(T *p, int n, float scale) {
         Vec::unpack(Vec::load(at), f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            f[i] *= scale;
+            f[i] = f[i] * scale * post;
         Vec::store(at, Vec::pack(f));
     }
     if (static_cast<int>(threadIdx.x) < c.rest) {
         T *at = p + c.rest_at(threadIdx.x);
-        *at = io_traits<T>::from_f(io_traits<T>::to_f(*at) * scale);
+        *at = io_traits<T>::from_f(io_traits<T>::to_f(*at) * scale * post);
     }
 }
 
@@ -218,15 +220,22 @@ __global__ void __launch_bounds__(kGradThreads, 4) s6_grad_scale_kernel(const __
         *a.norm_out = norm;
     // a NaN norm makes c NaN, and every gradient with it; an infinite one makes it 0; gradients
     // that are all zero stay so, with a bound and an eps of 0 too (c is 0 / 0 then)
-    const float c = a.max_norm / (norm + a.eps);
+    float c = a.max_norm / (norm + a.eps), post = 1.0f;
     if (c >= 1.0f || norm == 0.0f)
         return;
+    // a factor that float32 holds with fewer digits, or not at all, beside gradients large
+    // enough for products that it does hold: 2^64 of it here and 2^-64 behind
+    if (c < 0x1p-100f && norm <= FLT_MAX) {
+        c = static_cast<float>(static_cast<double>(a.max_norm) /
+                               (static_cast<double>(norm) + static_cast<double>(a.eps)) * 0x1p64);
+        post = 0x1p-64f;
+    }
     for (int k = t.chunks - 1 - static_cast<int>(blockIdx.x); k >= 0; k -= gridDim.x) {
         const GradSpan g = grad_span(t, k);
         if (g.bf16)
-            chunk_scale(static_cast<__nv_bfloat16 *>(g.p), g.n, c);
+            chunk_scale(static_cast<__nv_bfloat16 *>(g.p), g.n, c, post);
         else
-            chunk_scale(static_cast<float *>(g.p), g.n, c);
+            chunk_scale(static_cast<float *>(g.p), g.n, c, post);
     }
 }
 

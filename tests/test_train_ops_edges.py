@@ -439,3 +439,24 @@ def test_outputs_in_the_place_of_their_inputs(W):
                  lambda: S.s6_layernorm_bwd(x, s, buf[:700], rstd, dx=lo)):
         with pytest.raises(S.S6Error):
             call()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("size,max_norm,eps", [(1e30, 1e-14, 1e-6), (1e36, 1e-9, 0.0), (1e9, 1e-30, 1e-6), (3e36, 1.0, 0.0),
+                                               (1e30, 1e-10, 3e38), (1e38, 1e-3, 3.3e38), (1.0, 1e-37, 0.0), (1.0, 0.5, 0.0)])
+def test_clipping_by_factors_below_float32s_range(size, max_norm, eps, t):
+    """min(1, max_norm / (norm + eps)) where the factor, or norm + eps, leaves float32's range and
+    the scaled gradients do not."""
+    import torch
+    import selective_state_space_19_b200 as S
+    g = (size * torch.linspace(-1.0, 1.0, 5).double()).float().to(torch.bfloat16 if t == "bf16" else torch.float32)
+    a = g.double().numpy()
+    n = R.grad_norm([a])
+    want = a * (float(np.float32(max_norm)) / (n + float(np.float32(eps))))
+    dev = g.cuda()
+    norm = S.s6_clip_grad_norm([dev], max_norm, eps=eps)
+    assert abs(norm.item() - n) <= R.NORM_REL * n
+    half = R.HALF[t] if t == "bf16" else 0.0
+    # one rounding more (the second factor), and the smallest step of the storage type
+    step = 2.0 ** -133 if t == "bf16" else 2.0 ** -149
+    R.within(dev.double().cpu().numpy(), want, (R.SCALED_REL + R.U + half) * (1 + half) * np.abs(want) + step, "clipped")
