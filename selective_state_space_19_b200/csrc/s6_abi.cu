@@ -924,7 +924,7 @@ int fwd_ckpt_common(const s6_dims *dims, bool conv, const void *x, const float *
 
 extern "C" {
 
-int s6_version(void) { return (1 << 16) | 1; }
+int s6_version(void) { return (1 << 16) | 2; }
 
 const char *s6_status_string(int status) {
     switch (status) {

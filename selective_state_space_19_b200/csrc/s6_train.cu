@@ -83,17 +83,19 @@ struct Mem {
     }
 };
 
-// Refuses outputs that share memory with one another or with an input.
+// Refuses outputs that share memory with one another or with an input; the outputs are
+// listed first.
 template <size_t N>
 int check_apart(const Mem (&m)[N]) {
-    for (size_t i = 0; i < N; ++i)
-        for (size_t j = 0; j < N; ++j) {
-            if (i == j || m[i].use != kWritten || !m[i].p || !m[j].p || (m[j].use == kWritten && j < i))
-                continue;
-            const uint64_t a = reinterpret_cast<uintptr_t>(m[i].p), b = reinterpret_cast<uintptr_t>(m[j].p);
-            const uint64_t an = m[i].bytes(), bn = m[j].bytes();
-            const bool overlap = an && bn && (a <= b ? b - a < an : a - b < bn);
-            if (overlap && !(m[j].use == kEach && a == b && an == bn))
+    uint64_t at[N], size[N];
+    for (size_t i = 0; i < N; ++i) {
+        at[i] = reinterpret_cast<uintptr_t>(m[i].p);
+        size[i] = m[i].p ? m[i].bytes() : 0;
+    }
+    for (size_t i = 0; i < N && m[i].use == kWritten; ++i)  // these come first
+        for (size_t j = i + 1; j < N; ++j) {
+            const bool overlap = size[i] && size[j] && (at[i] <= at[j] ? at[j] - at[i] < size[i] : at[i] - at[j] < size[j]);
+            if (overlap && !(m[j].use == kEach && at[i] == at[j] && size[i] == size[j]))
                 return S6_ERR_INVALID_ARG;
         }
     return S6_OK;
