@@ -20,9 +20,12 @@
 // tokens at most) and float64 sums over the runs of a block's warps, which
 // s6_sum_parts_kernel then adds up over the blocks in a fixed order.
 //
-// Measured on one B200 (copies run at 6,521 GB/s): 16x8192x1536 f32 380 us = 97 %
-// of the copy rate, with bfloat16 x 356 = 87 %, all bfloat16 334 = 74 % (bound by
-// issue and the latency of 16 warps an SM); 8x256x1536 f32 14 us (latency).  Four
+// Measured on one B200 (copies run at 6,521 GB/s): 16x8192x1536 f32 379 us = 98 %
+// of the copy rate, with bfloat16 x 355 = 87 % (370 = 83 % where the inputs change
+// from call to call), all bfloat16 335 = 74 % (bound by issue and the latency of 16
+// warps an SM); 8x256x1536 f32 14 us = 40 % (its runs of 22 tokens take 25 steps and
+// walk 32, three of their four groups guarded); 16x2048x1535 f32 143 us = 65 % (half
+// of every pair is a zero).  Four
 // channels and groups of 4 tokens (the registers allow no more) took 457, 352,
 // 321 and 17 us; groups of 6 tokens 397, 384, 359 and 14.
 #pragma once
@@ -36,7 +39,7 @@ namespace s6 {
 constexpr int kConvBwdWarps = 4;
 constexpr int kConvBwdGroup = 8;   // tokens of the inner loop, each fetched one group ahead
 constexpr int kConvBwdPerSM = 4;   // resident blocks (128 registers a thread)
-constexpr int kConvBwdMaxRun = 1024;  // tokens that float32 sums run over: off by 6e-7 of the result at that length
+constexpr int kConvBwdMaxRun = 1024;  // tokens that float32 sums run over, at most; off by 5e-7 of the result in runs of 683
 
 struct ConvBwdArgs {
     int Bt, L, d;

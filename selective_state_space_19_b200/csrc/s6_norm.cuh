@@ -38,8 +38,13 @@
 // Measured on one B200 (copies run at 6,521 GB/s): 131072 rows of 384, a float32
 // stream and a bfloat16 branch: forward with the add 99 us = 94 % of the copy
 // rate, backward with the residual gradient 112 us = 96 %.  Wide rows: 8192x2560
-// f32 33 us forward and 47 backward (78, 82 %), bfloat16 21 and 41 (61, 63 %:
-// bound by issue, 18 and 30 instructions an element), 8191x2561 bfloat16 25.
+// f32 32 us forward and 47 backward (81, 82 %), bfloat16 21 and 41 (63, 63 %:
+// bound by issue, 18 and 30 instructions an element), 8191x2561 bfloat16 25 and 42
+// (52, 62 %).  Where the block's capacity is not the row's (768 of 1024 columns):
+// 32768x768 bfloat16 37 and 49 (42, 63 %), f32 39 and 55 (79, 85 %).  Narrow rows,
+// a chain of load, reductions and store with little to overlap: 131072x64 f32 14 and
+// 28 (72, 56 %), bfloat16 14 and 24 (36, 44 %).  The _wide forms: 4096x16384 f32 147
+// and 224 (56, 55 %), bfloat16 123 and 167 (33, 49 %).
 //
 // Vectors of 4 elements where the rows begin on one, else single elements:
 // rows of an odd width start anywhere, and the copies into shared memory keep

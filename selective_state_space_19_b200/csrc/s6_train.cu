@@ -158,6 +158,8 @@ struct NormBlockPlan {
 
 constexpr int kSmemSM = 227 * 1024, kSmemBlock = 2 * 1024;  // of an SM; a block's other shared memory, at most
 // by the registers: 128 a thread backward; forward 96 with four quads and 80 with fewer
+// (float32 rows with four quads, two at a time, take 122: of 128 threads four blocks fit
+// instead of five, 2 % of 16384x2048's time)
 constexpr int norm_block_per_sm(int threads, int quads, bool bwd) {
     return bwd ? 512 / threads : threads == 512 ? 1 : (quads == 4 ? 640 : 768) / threads;
 }
@@ -374,9 +376,13 @@ int64_t conv_bwd_blocks_y(int64_t d, int64_t channels) {
     return std::max<int64_t>(1, kConvBwdBlocks / ceil_div(d, channels));
 }
 
-// Runs that share the tokens out evenly, as many for each warp as every other: one
-// where the warps outnumber the sequences, else about four in all, and more where
-// they would be longer than kConvBwdMaxRun.
+// Runs of a sequence: as many as it has warps, rounded down; where the sequences
+// outnumber the warps, about four for each warp; and a multiple of that where they
+// would be longer than kConvBwdMaxRun.  They are even where the sequences divide the
+// warps (16x8192x1536: two runs for each).  Else warps are left over, or take a run
+// fewer: 16 sequences of 5120 channels have 28 warps a tile of channels, of which 16
+// work (16x100x5120 f32 29 us = 52 % of the copy rate), and above 1024 tokens 32 runs
+// in two rounds (16x2048x5120 412 us = 75 %).
 ConvBwdPlan conv_bwd_plan(int64_t Bt, int64_t L, int64_t d, int V) {
     ConvBwdPlan p;
     p.tiles = ceil_div(d, 32 * V);
