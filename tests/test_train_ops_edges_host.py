@@ -190,3 +190,11 @@ def test_build_makes_the_module_again_for_another_torch(tree, monkeypatch):
     B.build()
     assert calls() == ["cxx", "cxx", "nvcc"]  # the library is linked again, not compiled
     assert B.up_to_date()
+
+
+def test_the_recorded_traffic_is_of_the_present_scan_kernel():
+    """bench.py reports the DRAM bytes of the committed capture as long as the scan's sources are
+    those it was taken on; an edit of them asks for another capture."""
+    import bench
+    traffic, sha = bench.recorded_traffic()
+    assert sha == bench.kernel_source_sha() and traffic is not None and 1.4e9 < traffic < 1.7e9
