@@ -489,7 +489,8 @@ typedef struct {
  *
  * m, rstd and y come from the float32 sum x + r, before its rounding to s.  A
  * row's sum and the sum of its squared deviations are float32: above 3.4e38
- * they give NaN, or a rstd of 0.
+ * they give NaN, or a rstd of 0; squares below 1e-38 vanish, which an eps of 0
+ * turns into NaN or inf.
  */
 S6_API int s6_layernorm_fwd(const s6_norm_dims *dims, const void *x, const void *r, const float *w, const float *b,
                             void *s, void *y, float *mean, float *rstd, s6_stream_t stream);
